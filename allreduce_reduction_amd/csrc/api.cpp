@@ -398,7 +398,7 @@ const char* hbmc_status_string(hbmc_status_t status) {
   switch (status) {
     case HBMC_OK: return "success";
     case HBMC_ERR_INVALID_ARG: return "invalid argument";
-    case HBMC_ERR_UNSUPPORTED: return "unsupported collective for this algorithm (Reduce / Broadcast: RHD only; Flat, tree, hierarchical: AllReduce only)";
+    case HBMC_ERR_UNSUPPORTED: return "unsupported collective for this algorithm (Reduce / Broadcast: RHD only; Flat, tree, hierarchical: AllReduce only), or a size or type that an operator does not take";
     case HBMC_ERR_HIP: return "HIP error";
     case HBMC_ERR_NOMEM: return "out of memory";
     case HBMC_ERR_SCRATCH: return "the schedule's work-item table exceeds the no-allocation AllReduce's 2 MiB device array";

@@ -1,0 +1,348 @@
+// Distillation from a teacher's top logits over logits whose columns are dealt
+// out to the ranks, and the gradient of the logits (see hbmc_distill_loss).
+//
+// Both directions read the logits once: a wave takes a piece of a row's columns
+// on one rank, eight vectors a lane, all in flight at once.  The loss leaves
+// each piece's maximum and its sum of exponentials relative to that maximum,
+// and one wave a row joins them (log-sum-exp over the ranks) and adds the
+// teacher's few terms.  The gradient needs no join: a wave recomputes the
+// teacher's distribution, writes temperature * loss_grad * p over its piece and
+// then the columns that the teacher names.  HBM bounds both; the exponentials
+// come second (a quarter-rate instruction an element).
+#include <algorithm>
+
+#include "rowops.hpp"
+
+namespace hbmc {
+namespace dev {
+
+constexpr uint32_t kVectors = 8;  // of a lane in a piece
+constexpr float kLog2e = 1.44269504088896340736f;
+
+template <int DT>
+struct Piece {
+  static constexpr int VE = 16 / Width<DT>::bytes;
+  static constexpr uint32_t kElems = 64 * kVectors * VE;
+};
+
+// exp(x): the hardware's 2^x where the result is rounded to 16 bits or summed
+// over many columns (its error, about one unit of the last place beside the
+// product's rounding, is far below both), the accurate one for fp32 gradients.
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+__device__ __forceinline__ int64_t teacher_id(const DistillArgs& a, uint64_t i) {
+  return a.id_bytes == 8 ? reinterpret_cast<const int64_t*>(a.ids)[i] : reinterpret_cast<const int32_t*>(a.ids)[i];
+}
+
+// The i-th teacher entry: its column (vocab where it does not count) and its
+// logit over the temperature.
+__device__ __forceinline__ uint32_t teacher_entry(const DistillArgs& a, uint64_t i, float* t) {
+  const int64_t id = teacher_id(a, i);
+  float f[1];
+  if (a.teacher_dtype == kF32) Pack<kF32, 1>::widen(Pack<kF32, 1>::load(a.teacher + i * 4), f);
+  else if (a.teacher_dtype == kF16) Pack<kF16, 1>::widen(Pack<kF16, 1>::load(a.teacher + i * 2), f);
+  else Pack<kBF16, 1>::widen(Pack<kBF16, 1>::load(a.teacher + i * 2), f);
+  *t = f[0] / a.temperature;
+  return id >= 0 && id < static_cast<int64_t>(a.vocab) && f[0] != -__builtin_inff() ? static_cast<uint32_t>(id) : a.vocab;
+}
+
+// Maximum and sum of exponentials of a row's teacher entries; false where none counts.
+__device__ __forceinline__ bool teacher_stats(const DistillArgs& a, uint64_t row, uint32_t lane, float* top, float* sum) {
+  float m = -__builtin_inff(), s = 0.0f;
+  bool any = false;
+  for (uint32_t k = lane; k < a.top; k += 64) {
+    float t;
+    if (teacher_entry(a, row * a.top + k, &t) < a.vocab) {
+      any = true;
+      m = fmaxf(m, t);
+    }
+  }
+  if (__ballot(any) == 0) return false;
+  m = wave_max(m);
+  for (uint32_t k = lane; k < a.top; k += 64) {
+    float t;
+    if (teacher_entry(a, row * a.top + k, &t) < a.vocab) s += expf(t - m);
+  }
+  *top = m;
+  *sum = wave_sum(s);
+  return true;
+}
+
+template <int DT>
+__device__ __forceinline__ float logit_at(const DistillArgs& a, uint64_t row, uint32_t col) {
+  const uint32_t owner = col / a.seg;
+  const uint32_t cols = min(a.seg, a.vocab - owner * a.seg);
+  float f[1];
+  typedef Pack<DT, 1> K;
+  K::widen(K::load(a.logits[owner] + (row * cols + (col - owner * a.seg)) * K::E), f);
+  return f[0];
+}
+
+// Where a wave's piece lies: unit = row * parts + rank * pieces + piece.
+struct Place {
+  uint64_t row;
+  uint32_t rank, first, cols;  // first column on the rank, columns of the rank
+};
+__device__ __forceinline__ Place place_of(const DistillArgs& a, uint64_t unit, uint32_t elems) {
+  Place p;
+  p.row = unit / a.parts;
+  const uint32_t part = static_cast<uint32_t>(unit - p.row * a.parts);
+  p.rank = part / a.pieces;
+  p.first = (part - p.rank * a.pieces) * elems;
+  const uint64_t lo = uint64_t(p.rank) * a.seg;
+  p.cols = lo >= a.vocab ? 0 : min(a.seg, a.vocab - static_cast<uint32_t>(lo));
+  return p;
+}
+
+// A lane's columns of a piece: kVectors vectors, and for a piece that ends its
+// rank's columns the columns past the last whole vector, one a lane.  Columns
+// that are not there read as -infinity.
+template <int DT, bool WHOLE>
+struct Columns {
+  static constexpr int VE = Piece<DT>::VE;
+  typedef Pack<DT, VE> K;
+  typedef Pack<DT, 1> K1;
+  uint32_t at, end, rest;  // first column, end of the whole vectors, the lane's single column
+  bool has_rest;
+  typename K::raw v[kVectors];
+  uint32_t one;
+  __device__ __forceinline__ Columns(const Place& p, uint32_t lane) {
+    at = p.first + lane * VE;
+    end = p.cols / VE * VE;
+    rest = end + lane;
+    has_rest = !WHOLE && rest < p.cols;
+  }
+  __device__ __forceinline__ bool on(uint32_t k) const { return WHOLE || at + k * 64 * VE < end; }
+  __device__ __forceinline__ uint64_t byte(uint32_t k) const { return uint64_t(at + k * 64 * VE) * K::E; }
+  __device__ __forceinline__ void load(const unsigned char* row) {
+    constexpr uint32_t none = DT == kF32 ? 0xff800000u : (DT == kBF16 ? 0xff80ff80u : 0xfc00fc00u);
+#pragma unroll
+    for (uint32_t k = 0; k < kVectors; ++k) {
+      if constexpr (!WHOLE) v[k] = typename K::raw{none, none, none, none};
+      if (on(k)) v[k] = K::stream(row + byte(k));
+    }
+    one = none;
+    if (has_rest) one = K1::load(row + uint64_t(rest) * K::E);
+  }
+  __device__ __forceinline__ float single() const {
+    float f[1];
+    K1::widen(one, f);
+    return f[0];
+  }
+};
+
+template <int DT, bool WHOLE>
+__device__ __forceinline__ float2 piece_stats(const Place& p, const unsigned char* row, uint32_t lane, float inv) {
+  constexpr int VE = Piece<DT>::VE;
+  typedef Pack<DT, VE> K;
+  Columns<DT, WHOLE> c(p, lane);
+  c.load(row);
+  float m = WHOLE ? -__builtin_inff() : c.single();
+#pragma unroll
+  for (uint32_t k = 0; k < kVectors; ++k) {
+    float f[VE];
+    K::widen(c.v[k], f);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) m = fmaxf(m, f[i]);
+  }
+  m = wave_max(m);
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  float s = WHOLE ? 0.0f : exp_fast((c.single() - base) * inv);
+#pragma unroll
+  for (uint32_t k = 0; k < kVectors; ++k) {
+    float f[VE];
+    K::widen(c.v[k], f);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) s += exp_fast((f[i] - base) * inv);
+  }
+  return float2{m, wave_sum(s)};
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void distill_part_kernel(DistillArgs a) {
+  const uint32_t lane = threadIdx.x & 63;
+  const uint64_t units = a.rows * a.parts;
+  const float inv = 1.0f / a.temperature;
+  for (uint64_t unit = uint64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); unit < units; unit += uint64_t(gridDim.x) * 4) {
+    const Place p = place_of(a, unit, Piece<DT>::kElems);
+    const unsigned char* row = a.logits[p.rank] + p.row * p.cols * Width<DT>::bytes;
+    float2 r = {-__builtin_inff(), 0.0f};
+    if (p.first + Piece<DT>::kElems <= p.cols) r = piece_stats<DT, true>(p, row, lane, inv);
+    else if (p.first < p.cols) r = piece_stats<DT, false>(p, row, lane, inv);
+    if (lane == 0) a.partial[unit] = r;
+  }
+}
+
+// Joins a row's pieces and adds the teacher's terms: one wave a row.
+template <int DT>
+__global__ __launch_bounds__(256) void distill_join_kernel(DistillArgs a) {
+  const uint32_t lane = threadIdx.x & 63;
+  for (uint64_t row = uint64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); row < a.rows; row += uint64_t(gridDim.x) * 4) {
+    const float2* part = a.partial + row * a.parts;
+    const float inv = 1.0f / a.temperature;
+    float m = -__builtin_inff(), s = 0.0f;
+    for (uint32_t i = lane; i < a.parts; i += 64) m = fmaxf(m, part[i].x);
+    m = wave_max(m);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    // a piece of -inf alone has the sum 0 (or NaN)
+    for (uint32_t i = lane; i < a.parts; i += 64) s += part[i].y * expf((part[i].x == -__builtin_inff() ? 0.0f : part[i].x - base) * inv);
+    s = wave_sum(s);
+    const float lse = base * inv + logf(s);
+    float top, sum, loss = 0.0f;
+    if (teacher_stats(a, row, lane, &top, &sum)) {
+      const float log_sum = logf(sum);
+      for (uint32_t k = lane; k < a.top; k += 64) {
+        float t;
+        const uint32_t col = teacher_entry(a, row * a.top + k, &t);
+        if (col < a.vocab) {
+          const float q = expf(t - top) / sum;
+          const float log_p = lse == -__builtin_inff() ? lse : logit_at<DT>(a, row, col) / a.temperature - lse;
+          const float term = q * ((t - top) - log_sum - log_p);
+          loss += q == 0.0f ? 0.0f : term;
+        }
+      }
+      loss = wave_sum(loss) * a.temperature * a.temperature;
+    }
+    if (lane == 0) {
+      a.loss[row] = loss;
+      a.lse[row] = lse;
+    }
+  }
+}
+
+// A teacher entry of a wave's piece: its column on the rank, its q, and the
+// bits to store there.
+struct Entry {
+  uint32_t col;
+  float q;
+  uint32_t bits;
+};
+
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p, uint32_t lane, Entry* list) {
+  constexpr int VE = Piece<DT>::VE;
+  typedef Pack<DT, VE> K;
+  typedef Pack<DT, 1> K1;
+  const uint64_t off = p.row * p.cols * K::E;
+  const unsigned char* row = a.logits[p.rank] + off;
+  unsigned char* out = a.grads[p.rank] + off;
+  const float given = a.loss_grad[p.row], by = given * a.temperature, lse = a.lse[p.row];
+  const float inv = 1.0f / a.temperature;
+  Columns<DT, WHOLE> c(p, lane);
+  float top = 0.0f, sum = 1.0f;
+  bool some = given != 0.0f;
+  if (some) {
+    c.load(row);
+    some = teacher_stats(a, p.row, lane, &top, &sum);
+  }
+  if (!some) {
+#pragma unroll
+    for (uint32_t k = 0; k < kVectors; ++k)
+      if (c.on(k)) K::store(out + c.byte(k), typename K::raw{});
+    if (c.has_rest) K1::store(out + uint64_t(c.rest) * K::E, 0);
+    return;
+  }
+  const auto prob = [&](float z) {
+    if (lse == -__builtin_inff()) return 0.0f;
+    const float x = z * inv - lse;
+    if constexpr (DT == kF32) return expf(x);
+    else return exp_fast(x);
+  };
+  const uint32_t lo = p.rank * a.seg;
+  uint32_t n = 0;
+  for (uint32_t k0 = 0; k0 < a.top; k0 += 64) {
+    float t = 0.0f;
+    const uint32_t k = k0 + lane;
+    const uint32_t col = k < a.top ? teacher_entry(a, p.row * a.top + k, &t) : a.vocab;
+    const bool in = col < a.vocab && col >= lo + p.first && col - lo - p.first < Piece<DT>::kElems && col - lo < p.cols;
+    const uint64_t who = __ballot(in);
+    if (in) {
+      Entry& e = list[n + __popcll(who & ((uint64_t(1) << lane) - 1))];
+      e.col = col - lo;
+      e.q = expf(t - top) / sum;
+    }
+    n += __popcll(who);
+  }
+  wave_order();
+  // the values at the named columns, from the logits before they are written
+  // over (grads may be logits); a column named twice gets one value twice
+  for (uint32_t e = lane; e < n; e += 64) {
+    const uint32_t col = list[e].col;
+    float q = 0.0f, z[1];
+    for (uint32_t j = 0; j < n; ++j) q += list[j].col == col ? list[j].q : 0.0f;
+    K1::widen(K1::load(row + uint64_t(col) * K::E), z);
+    const float value[1] = {by * (prob(z[0]) - q)};
+    list[e].bits = K1::narrow(value);
+  }
+  wave_order();
+#pragma unroll
+  for (uint32_t k = 0; k < kVectors; ++k) {
+    float f[VE];
+    K::widen(c.v[k], f);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) f[i] = by * prob(f[i]);
+    if (c.on(k)) K::store(out + c.byte(k), K::narrow(f));
+  }
+  if (c.has_rest) {
+    const float f[1] = {by * prob(c.single())};
+    K1::store(out + uint64_t(c.rest) * K::E, K1::narrow(f));
+  }
+  wave_order();  // the same wave's stores to the same places follow
+  for (uint32_t e = lane; e < n; e += 64) K1::store(out + uint64_t(list[e].col) * K::E, list[e].bits);
+  wave_order();  // the list is free again
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void distill_grad_kernel(DistillArgs a) {
+  extern __shared__ Entry lists[];  // [4][top]
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint64_t units = a.rows * a.parts;
+  for (uint64_t unit = uint64_t(blockIdx.x) * 4 + wave; unit < units; unit += uint64_t(gridDim.x) * 4) {
+    const Place p = place_of(a, unit, Piece<DT>::kElems);
+    if (p.first + Piece<DT>::kElems <= p.cols) piece_grad<DT, true>(a, p, lane, lists + wave * a.top);
+    else if (p.first < p.cols) piece_grad<DT, false>(a, p, lane, lists + wave * a.top);
+  }
+}
+
+}  // namespace dev
+
+namespace {
+
+using namespace dev;
+
+hipError_t go(const void* f, uint64_t groups, uint32_t shared, void** argv, hipStream_t stream) {
+  return hipLaunchKernel(f, dim3(static_cast<uint32_t>(std::min<uint64_t>(groups, 1 << 22))), dim3(256), argv, shared, stream);
+}
+
+#define HBMC_BY_TYPE(kernel)                                                  \
+  (dtype == kF32   ? reinterpret_cast<const void*>(&kernel<kF32>)             \
+   : dtype == kF16 ? reinterpret_cast<const void*>(&kernel<kF16>)             \
+                   : reinterpret_cast<const void*>(&kernel<kBF16>))
+
+}  // namespace
+
+uint32_t distill_pieces(int dtype, uint64_t seg) {
+  const uint32_t elems = dtype == kF32 ? Piece<kF32>::kElems : Piece<kF16>::kElems;
+  return static_cast<uint32_t>((seg + elems - 1) / elems);
+}
+
+hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream) {
+  void* argv[] = {const_cast<DistillArgs*>(&a)};
+  const hipError_t e = go(HBMC_BY_TYPE(distill_part_kernel), (a.rows * a.parts + 3) / 4, 0, argv, stream);
+  if (e != hipSuccess) return e;
+  return go(HBMC_BY_TYPE(distill_join_kernel), (a.rows + 3) / 4, 0, argv, stream);
+}
+
+hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t stream) {
+  void* argv[] = {const_cast<DistillArgs*>(&a)};
+  return go(HBMC_BY_TYPE(distill_grad_kernel), (a.rows * a.parts + 3) / 4, 4 * a.top * sizeof(Entry), argv, stream);
+}
+
+#undef HBMC_BY_TYPE
+
+}  // namespace hbmc

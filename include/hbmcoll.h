@@ -499,6 +499,142 @@ hbmc_status_t hbmc_graph_build(hbmc_graph_t graph);
 hbmc_status_t hbmc_graph_launch(hbmc_graph_t graph, void* stream);
 hbmc_status_t hbmc_graph_destroy(hbmc_graph_t graph);
 
+/*
+ * Operators of a model at the places where its own row work meets a
+ * collective over the ranks: the norms at a block's end over the ranks'
+ * partial sums, the embedding whose rows are dealt out to the ranks, and the
+ * loss over logits whose columns are dealt out to the ranks.  Each does the
+ * collective's additions and copies itself, in one pass over the ranks'
+ * buffers; the communicator gives the number of ranks P (its algorithm plays
+ * no part: sums over ranks are taken in 32 bits, ranks ascending, and rounded
+ * once).  n rows or columns are dealt out as the collectives deal out
+ * elements: rank r owns [r * ceil(n / P), min(n, (r + 1) * ceil(n / P))).
+ *
+ * Rules common to the calls below, beyond those at the top:
+ *   - matrices are contiguous, row after row, aligned to their element size
+ *     (16-byte aligned rows are fastest); dtype is HBMC_FP32, HBMC_FP16 or
+ *     HBMC_BF16; gradients of weights and per-row statistics are fp32;
+ *   - a pointer whose rank owns nothing may be NULL; a buffer that is written
+ *     must not overlap any other buffer of the call unless stated;
+ *   - `workspace` is scratch memory of at least the bytes the matching
+ *     ..._workspace call (host only) reports, 16-byte aligned, the caller's
+ *     own (NULL for none), free to reuse once the call's work on `stream` is done.  Calls that
+ *     may run at the same time, replayed graphs included, need one each;
+ *   - nothing is allocated, cached or synchronised: every call may be
+ *     captured into a graph, the first one included;
+ *   - the same inputs give the same bits on every run.
+ */
+
+/*
+ * The norms before and after a block's end, with its gate and residual scale.
+ * For every row t of `rows` rows of `width` elements (at most 16384):
+ *   s = sum over ranks p of parts[p][t]
+ *   n = s / sqrt(mean(s^2) + post_eps) * post_weight    (s without post_weight)
+ *   h = residual[t] + scale * gate[t / gate_rows] * n   (no gate: 1)
+ *   out[p][t] = h / sqrt(mean(h^2) + pre_eps) * pre_weight, on every rank p
+ * with every intermediate in 32 bits.  gate has ceil(rows / gate_rows) rows.
+ */
+typedef struct {
+  size_t rows, width;
+  size_t gate_rows;        /* rows that share a gate row (>= 1 with a gate, else ignored) */
+  hbmc_dtype_t dtype;      /* of every matrix, weight and gate                            */
+  float scale, pre_eps, post_eps;
+  const void* pre_weight;  /* [width]                                                     */
+  const void* post_weight; /* [width], or NULL: no norm after the block                   */
+  const void* gate;        /* [ceil(rows / gate_rows)][width], or NULL                    */
+} hbmc_norm_t;
+
+/* parts[p], out[p]: [rows][width] on each rank.  residual[r], residual_out[r],
+ * sums[r]: the rows that rank r owns.  Writes out, residual_out (h rounded)
+ * and, unless sums is NULL, sums (s rounded: what the gradient reads).
+ * out[p] may be parts[p], residual_out[r] may be residual[r]. */
+hbmc_status_t hbmc_reduce_norm(hbmc_comm_t comm, const hbmc_norm_t* norm, const void* const parts[],
+                               const void* const residual[], void* const residual_out[], void* const out[],
+                               void* const sums[], void* stream);
+
+/* The gradient.  out_grads[p]: the gradient that rank p has for out (they are
+ * added); hidden[r]: residual_out; sums[r]: as the forward call wrote them
+ * (NULL allowed without post_weight and gate); residual_grad_in[r]: the
+ * gradient of residual_out from later use, or NULL.  Writes part_grads[p] (the
+ * gradient of parts[p], the same on every rank), residual_grad[r] (of
+ * residual), and in fp32, summed over all rows, pre_weight_grad [width],
+ * post_weight_grad [width] and gate_grad [ceil(rows / gate_rows)][width] (the
+ * last two exactly where post_weight and gate are given).  part_grads[p] may
+ * be out_grads[p], residual_grad[r] may be residual_grad_in[r].  rows == 0
+ * writes zero weight gradients. */
+hbmc_status_t hbmc_reduce_norm_grad_workspace(hbmc_comm_t comm, const hbmc_norm_t* norm, size_t* bytes);
+hbmc_status_t hbmc_reduce_norm_grad(hbmc_comm_t comm, const hbmc_norm_t* norm, const void* const out_grads[],
+                                    const void* const hidden[], const void* const sums[],
+                                    const void* const residual_grad_in[], void* const part_grads[],
+                                    void* const residual_grad[], float* pre_weight_grad, float* post_weight_grad,
+                                    float* gate_grad, void* workspace, size_t workspace_bytes, void* stream);
+
+/* An embedding of `vocab` rows (1 .. 2^30) of `width` elements, rank r holding
+ * the rows it owns. */
+typedef struct {
+  size_t vocab, width;
+  hbmc_dtype_t dtype;
+  int id_bytes;  /* width of the token ids: 4 or 8 (signed) */
+  float scale;
+} hbmc_embedding_t;
+
+/* out[p][t] = scale * row ids[p][t] of the table, for the tokens[p] (below
+ * 2^26) tokens of each rank p; ids outside [0, vocab) give rows of zeros.
+ * tables[r]: the rows that rank r owns.  The ranks' ids may be one buffer. */
+hbmc_status_t hbmc_embedding(hbmc_comm_t comm, const hbmc_embedding_t* emb, const void* const tables[],
+                             const void* const ids[], const size_t tokens[], void* const out[], void* stream);
+
+/* The table's gradient: row v of the table receives scale * the sum of
+ * out_grads[p][t] over every rank p and token t with ids[p][t] == v (tokens
+ * sorted by id; within an id by rank, then token; 32-bit sums in a grouping
+ * fixed by the sizes), rounded once to grad_dtype (HBMC_FP32 or emb->dtype) and
+ * with `accumulate` added to what table_grads holds, whose other rows are then
+ * left untouched.  Without it every row is written, zeros where no token has
+ * its id. */
+hbmc_status_t hbmc_embedding_grad_workspace(hbmc_comm_t comm, const hbmc_embedding_t* emb, const size_t tokens[],
+                                            size_t* bytes);
+hbmc_status_t hbmc_embedding_grad(hbmc_comm_t comm, const hbmc_embedding_t* emb, const void* const out_grads[],
+                                  const void* const ids[], const size_t tokens[], void* const table_grads[],
+                                  hbmc_dtype_t grad_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/*
+ * Distillation from a teacher's top logits.  Rank r holds logits[r], the
+ * columns of [rows][vocab] that it owns, as a contiguous [rows][columns of r].
+ * Each row has `top` (1 .. 1024) teacher logits and their columns; an entry
+ * whose id is outside [0, vocab) or whose logit is -infinity does not count.
+ * With q = softmax(teacher / temperature) over a row's counting entries and
+ * p = softmax(logits / temperature) over the row,
+ *   loss = temperature^2 * sum_k q_k * (log q_k - log p[id_k])
+ * and 0 for a row without counting entries; the same column may be named
+ * twice.  vocab is at most 2^30.
+ */
+typedef struct {
+  size_t rows, vocab, top;
+  hbmc_dtype_t dtype;         /* of the logits and their gradients             */
+  hbmc_dtype_t teacher_dtype; /* fp32, fp16 or bf16                            */
+  int id_bytes;               /* 4 or 8 (signed)                               */
+  float temperature;          /* > 0                                           */
+  const void* teacher_logits; /* [rows][top]                                   */
+  const void* teacher_ids;    /* [rows][top]                                   */
+} hbmc_distill_t;
+
+/* Writes loss [rows] and lse [rows], log sum_j exp(logits_j / temperature).
+ * A row whose logits are all -infinity has lse -infinity and, where an entry
+ * counts, loss +infinity. */
+hbmc_status_t hbmc_distill_loss_workspace(hbmc_comm_t comm, const hbmc_distill_t* distill, size_t* bytes);
+hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
+                                float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* logit_grads[r][t][j] = loss_grad[t] * temperature * (p_j - the sum of q_k
+ * over the entries with column j), from the forward call's lse; zeros for a
+ * row whose loss_grad is zero or that has no counting entry, whatever its
+ * logits hold; p is zero in a row whose lse is -infinity.  logit_grads[r] may
+ * be logits[r]. */
+hbmc_status_t hbmc_distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
+                                     const float* lse, const float* loss_grad, void* const logit_grads[],
+                                     void* stream);
+
 /* Static text for a status code. */
 const char* hbmc_status_string(hbmc_status_t status);
 
