@@ -1,7 +1,7 @@
 """Python binding of the hbmcoll C ABI (``include/hbmcoll.h``).
 
-Argument marshalling only: every step of a collective runs in the gfx950
-kernels of ``libhbmcoll.so``.  PyTorch supplies device memory and the stream.
+Argument marshalling only: every step of a collective and every operator runs
+in the gfx950 kernels of ``libhbmcoll.so``.  PyTorch supplies device memory and the stream.
 There is no fallback: if the library is missing, loading fails loudly.
 """
 from __future__ import annotations
@@ -252,105 +252,36 @@ def _stream(stream) -> int:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+_operators = None
+
+
+def load_operators():
+    """The operators' binding (``_native.so``: argument checks, then the C ABI; raises if it is not built)."""
+    global _operators
+    if _operators is None:
+        import torch  # noqa: F401 - the module uses torch's libraries
+        from . import _native
+        _operators = _native
+    return _operators
+
+
 def _current_device() -> int:
     import torch
     return torch.cuda.current_device()
-
-
-_ARRAYS = {}  # ctypes pointer-array types by length
-
-
-def _array(n):
-    t = _ARRAYS.get(n)
-    if t is None:
-        t = _ARRAYS[n] = ctypes.c_void_p * n
-    return t
-
-
-class _Call:
-    """Argument checks of one operator call: every tensor lies on the current
-    device, is contiguous, and has the type and shape the call gives it."""
-
-    __slots__ = ("dev", "P")
-
-    def __init__(self, P):
-        self.P = P
-        self.dev = _current_device()
-
-    def tensor(self, t, dtype, shape, what):
-        """Address of one tensor of exactly this shape."""
-        if t.dtype is not dtype or t.get_device() != self.dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {shape} on device {self.dev} is needed, "
-                             f"got {t.dtype} {tuple(t.shape)} on device {t.get_device()}")
-        return t.data_ptr()
-
-    def ranks(self, bufs, dtype, shapes, what):
-        """Addresses of the ranks' tensors: a list of P tensors with these
-        shapes (one for all, or one each), or one tensor [P, ...] of them."""
-        P, dev = self.P, self.dev
-        same = type(shapes) is tuple
-        if hasattr(bufs, "data_ptr"):
-            if not same:
-                raise TypeError(f"{what}: the ranks' tensors differ in shape, so a list of them is needed")
-            base = self.tensor(bufs, dtype, (P,) + shapes, what)
-            step = bufs.element_size()
-            for n in shapes:
-                step *= n
-            return _array(P)(*[base + r * step for r in range(P)])
-        if len(bufs) != P:
-            raise ValueError(f"{what}: {P} tensors are needed, got {len(bufs)}")
-        for r, t in enumerate(bufs):
-            if t.dtype is not dtype or t.get_device() != dev or t.shape != (shapes if same else shapes[r]) \
-                    or not t.is_contiguous():
-                raise ValueError(
-                    f"{what}: rank {r} needs a contiguous {dtype} tensor of shape {shapes if same else shapes[r]} on "
-                    f"device {dev}, got {t.dtype} {tuple(t.shape)} on device {t.get_device()}")
-        return _array(P)(*[t.data_ptr() for t in bufs])
-
-    def rows(self, n, width):
-        """Shapes of the ranks' rows of an [n, width] matrix (the ceiling split)."""
-        each = -(-n // self.P)
-        return [(min(each, max(0, n - r * each)), width) for r in range(self.P)]
-
-
-def _float_type(t, what):
-    """Library code of a floating tensor's type."""
-    name = _torch_dtypes().get(t.dtype)
-    if name not in ("fp32", "fp16", "bf16"):
-        raise TypeError(f"{what}: unsupported tensor dtype {t.dtype}")
-    return DTYPE[name]
-
-
-def _first(bufs, what):
-    """The first rank's tensor."""
-    if len(bufs) == 0:
-        raise ValueError(f"{what}: no tensors")
-    return bufs[0]
-
-
-def _id_type(t, what):
-    import torch
-    if t.dtype is not torch.int32 and t.dtype is not torch.int64:
-        raise TypeError(f"{what}: ids are int32 or int64, got {t.dtype}")
-    return 4 if t.dtype is torch.int32 else 8
 
 
 def _scratch(nbytes, dev, stream):
     """Workspace from torch's allocator, on the stream that uses it (so that
     it is handed out again only to work after this call's)."""
     import torch
-    if nbytes == 0:
-        return None, 0
     if stream is not None:
         raw = int(getattr(stream, "cuda_stream", stream))
         if raw != torch.cuda.current_stream(dev).cuda_stream:
             # raw handle 0 is the default stream, which torch does not wrap as an external one
             on = torch.cuda.default_stream(dev) if raw == 0 else torch.cuda.ExternalStream(raw, device=dev)
             with torch.cuda.stream(on):
-                t = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-            return t, t.data_ptr()
-    t = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{dev}")
-    return t, t.data_ptr()
+                return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
 
 
 class Comm:
@@ -425,6 +356,16 @@ class Comm:
                                              first, last, _stream(stream)), "hbmc_run_steps")
 
     # -- operators over the ranks
+    def _operate(self, name, stream, *args, scratch=False):
+        """One call of the binding: every tensor must lie on the current device,
+        be contiguous and have the type and shape that the call gives it."""
+        dev = _current_device()
+        if scratch:
+            args += (lambda nbytes: _scratch(nbytes, dev, stream),)
+        rc = getattr(load_operators(), name)(self._h.value, self.P, dev, _stream(stream), *args)
+        if rc != OK:
+            raise HbmcError(rc, "hbmc_" + name)
+
     def reduce_norm(self, parts, residual, out, pre_weight, *, residual_out=None, sums=None, post_weight=None,
                     gate=None, scale=1.0, eps=1e-6, post_eps=None, stream=None):
         """The norms before and after a block's end (see hbmc_reduce_norm).
@@ -435,17 +376,10 @@ class Comm:
         parts; n = s / rms(s) * post_weight (or s); h = residual + scale *
         gate * n; residual_out = h; out = h / rms(h) * pre_weight on every
         rank; sums, where given, receives s for the gradient.  gate is
-        [groups, width], each row for rows / groups rows in turn."""
-        c = _Call(self.P)
-        first = _first(parts, "parts")
-        dt = first.dtype
-        norm = self._norm(c, _float_type(first, "parts"), first, pre_weight, post_weight, gate, scale, eps, post_eps)
-        full, segs = (norm.rows, norm.width), c.rows(norm.rows, norm.width)
-        res = c.ranks(residual, dt, segs, "residual")
-        res_out = res if residual_out is None else c.ranks(residual_out, dt, segs, "residual_out")
-        _check(load_library().hbmc_reduce_norm(
-            self._h, norm, c.ranks(parts, dt, full, "parts"), res, res_out, c.ranks(out, dt, full, "out"),
-            None if sums is None else c.ranks(sums, dt, segs, "sums"), _stream(stream)), "hbmc_reduce_norm")
+        [groups, width], each row for rows / groups rows in turn; post_eps
+        defaults to eps."""
+        self._operate("reduce_norm", stream, parts, residual, residual_out, out, sums, pre_weight, post_weight, gate, scale,
+                      eps, post_eps)
 
     def reduce_norm_grad(self, out_grads, hidden, part_grads, residual_grad, pre_weight, pre_weight_grad, *, sums=None,
                          residual_grad_in=None, post_weight=None, post_weight_grad=None, gate=None, gate_grad=None,
@@ -457,50 +391,9 @@ class Comm:
         gate); residual_grad_in: the gradient of residual_out from later use.
         Writes part_grads (every rank's), residual_grad, and the fp32
         pre_weight_grad, post_weight_grad and gate_grad."""
-        import torch
-        c = _Call(self.P)
-        first = _first(out_grads, "out_grads")
-        dt = first.dtype
-        norm = self._norm(c, _float_type(first, "out_grads"), first, pre_weight, post_weight, gate, scale, eps, post_eps)
-        n, width = norm.rows, norm.width
-        if (post_weight is None) != (post_weight_grad is None) or (gate is None) != (gate_grad is None):
-            raise ValueError("post_weight_grad and gate_grad go with post_weight and gate")
-        if sums is None and not (post_weight is None and gate is None):
-            raise ValueError("the forward call's sums are needed with post_weight or gate")
-        full, segs = (n, width), c.rows(n, width)
-        L = load_library()
-        nbytes = ctypes.c_size_t()
-        _check(L.hbmc_reduce_norm_grad_workspace(self._h, norm, ctypes.byref(nbytes)), "hbmc_reduce_norm_grad_workspace")
-        args = (c.ranks(out_grads, dt, full, "out_grads"), c.ranks(hidden, dt, segs, "hidden"),
-                None if sums is None else c.ranks(sums, dt, segs, "sums"),
-                None if residual_grad_in is None else c.ranks(residual_grad_in, dt, segs, "residual_grad_in"),
-                c.ranks(part_grads, dt, full, "part_grads"), c.ranks(residual_grad, dt, segs, "residual_grad"),
-                c.tensor(pre_weight_grad, torch.float32, (width,), "pre_weight_grad"),
-                None if post_weight is None else c.tensor(post_weight_grad, torch.float32, (width,), "post_weight_grad"),
-                None if gate is None else c.tensor(gate_grad, torch.float32, (gate.shape[0], width), "gate_grad"))
-        keep, ws = _scratch(nbytes.value, c.dev, stream)
-        _check(L.hbmc_reduce_norm_grad(self._h, norm, *args, ws, nbytes.value, _stream(stream)), "hbmc_reduce_norm_grad")
-
-    @staticmethod
-    def _norm(c, code, first, pre_weight, post_weight, gate, scale, eps, post_eps):
-        if first.dim() != 2:
-            raise ValueError(f"each rank's tensor is [rows, width], got {tuple(first.shape)}")
-        n, width = first.shape
-        dt = first.dtype
-        gate_rows = 1
-        if gate is not None:
-            groups = gate.shape[0]
-            if groups == 0 or n % groups:
-                if n or groups:
-                    raise ValueError(f"gate: {groups} rows do not divide {n} rows evenly")
-            else:
-                gate_rows = max(1, n // groups)
-            gate = c.tensor(gate, dt, (groups, width), "gate")
-            if groups == 0:
-                gate = None
-        return Norm(n, width, gate_rows, code, scale, eps, eps if post_eps is None else post_eps,
-                    c.tensor(pre_weight, dt, (width,), "pre_weight"),
-                    None if post_weight is None else c.tensor(post_weight, dt, (width,), "post_weight"), gate)
+        self._operate("reduce_norm_grad", stream, out_grads, hidden, part_grads, residual_grad, pre_weight, pre_weight_grad,
+                      sums, residual_grad_in, post_weight, post_weight_grad, gate, gate_grad, scale, eps, post_eps,
+                      scratch=True)
 
     def embedding(self, tables, ids, out, *, scale=1.0, stream=None):
         """out[p][t] = scale * row ids[p][t] of the table (see hbmc_embedding).
@@ -508,59 +401,14 @@ class Comm:
         tables: the rows of the vocabulary each rank owns; ids: each rank's
         token ids, int32 or int64, one dimension; out: each rank's [tokens,
         width].  Ids outside the vocabulary give zeros."""
-        c = _Call(self.P)
-        emb, tabs, idp, tokens, dt = self._embedding(c, tables, ids, None, scale)
-        outs = c.ranks(out, dt, [(n, emb.width) for n in tokens], "out") if not hasattr(out, "data_ptr") else \
-            c.ranks(out, dt, (tokens[0], emb.width), "out")
-        _check(load_library().hbmc_embedding(self._h, emb, tabs, idp, tokens, outs, _stream(stream)), "hbmc_embedding")
+        self._operate("embedding", stream, tables, ids, out, scale)
 
     def embedding_grad(self, out_grads, ids, table_grads, *, scale=1.0, accumulate=False, stream=None):
         """The gradient of embedding's table (see hbmc_embedding_grad): the sum
         of out_grads' rows by id, times scale, into the rows each rank owns
         (fp32 or out_grads' type); added to them with accumulate, else every
         row is written."""
-        c = _Call(self.P)
-        first = _first(out_grads, "out_grads")
-        code = _float_type(first, "out_grads")
-        emb, grads, idp, tokens, gdt = self._embedding(c, table_grads, ids, code, scale)
-        if first.dim() != 2 or first.shape[1] != emb.width:
-            raise ValueError(f"out_grads: [tokens, {emb.width}] tensors are needed, got {tuple(first.shape)}")
-        gcode = _float_type(_first(table_grads, "table_grads"), "table_grads")
-        if gcode != code and gcode != DTYPE["fp32"]:
-            raise TypeError("table_grads are fp32 or of out_grads' type")
-        dt = first.dtype
-        rows = c.ranks(out_grads, dt, [(n, emb.width) for n in tokens], "out_grads") \
-            if not hasattr(out_grads, "data_ptr") else c.ranks(out_grads, dt, (tokens[0], emb.width), "out_grads")
-        L = load_library()
-        nbytes = ctypes.c_size_t()
-        _check(L.hbmc_embedding_grad_workspace(self._h, emb, tokens, ctypes.byref(nbytes)),
-               "hbmc_embedding_grad_workspace")
-        keep, ws = _scratch(nbytes.value, c.dev, stream)
-        _check(L.hbmc_embedding_grad(self._h, emb, rows, idp, tokens, grads, gcode, 1 if accumulate else 0, ws,
-                                     nbytes.value, _stream(stream)), "hbmc_embedding_grad")
-
-    def _embedding(self, c, tables, ids, code, scale):
-        first = _first(tables, "tables")
-        if first.dim() != 2:
-            raise ValueError(f"each rank's rows are [rows, width], got {tuple(first.shape)}")
-        width = first.shape[1]
-        if hasattr(tables, "data_ptr"):
-            vocab = tables.shape[0] * tables.shape[1]
-            tabs = c.ranks(tables, first.dtype, (first.shape[0], width), "tables")
-        else:
-            vocab = sum([t.shape[0] for t in tables])
-            tabs = c.ranks(tables, first.dtype, c.rows(vocab, width), "tables")
-        one = _first(ids, "ids")
-        if len(ids) != self.P:
-            raise ValueError(f"ids: {self.P} tensors are needed, got {len(ids)}")
-        tokens = (ctypes.c_size_t * self.P)(*[t.numel() for t in ids])
-        if hasattr(ids, "data_ptr"):
-            idp = c.ranks(ids, one.dtype, (tokens[0],), "ids")
-        else:
-            idp = c.ranks(ids, one.dtype, [(n,) for n in tokens], "ids")
-        if code is None:
-            code = _float_type(first, "tables")
-        return Embedding(vocab, width, code, _id_type(one, "ids"), scale), tabs, idp, tokens, first.dtype
+        self._operate("embedding_grad", stream, out_grads, ids, table_grads, scale, accumulate, scratch=True)
 
     def distill_loss(self, logits, teacher_logits, teacher_ids, loss, lse, *, temperature=1.0, stream=None):
         """temperature^2 * KL(teacher || student) of each row, into loss, and
@@ -570,44 +418,14 @@ class Comm:
         logits: the columns of [rows, vocab] each rank owns; teacher_logits,
         teacher_ids: [rows, top], the teacher's logits and their columns
         (int32 or int64; negative: not there)."""
-        import torch
-        c = _Call(self.P)
-        d, ptrs, _, _ = self._distill(c, logits, teacher_logits, teacher_ids, temperature)
-        out = (c.tensor(loss, torch.float32, (d.rows,), "loss"), c.tensor(lse, torch.float32, (d.rows,), "lse"))
-        L = load_library()
-        nbytes = ctypes.c_size_t()
-        _check(L.hbmc_distill_loss_workspace(self._h, d, ctypes.byref(nbytes)), "hbmc_distill_loss_workspace")
-        keep, ws = _scratch(nbytes.value, c.dev, stream)
-        _check(L.hbmc_distill_loss(self._h, d, ptrs, *out, ws, nbytes.value, _stream(stream)), "hbmc_distill_loss")
+        self._operate("distill_loss", stream, logits, teacher_logits, teacher_ids, loss, lse, temperature, scratch=True)
 
     def distill_loss_grad(self, logits, teacher_logits, teacher_ids, lse, loss_grad, logit_grads, *, temperature=1.0,
                           stream=None):
         """The gradient of distill_loss: loss_grad [rows] (fp32) into
         logit_grads, shaped as logits and allowed to be them."""
-        import torch
-        c = _Call(self.P)
-        d, ptrs, dt, shapes = self._distill(c, logits, teacher_logits, teacher_ids, temperature)
-        _check(load_library().hbmc_distill_loss_grad(
-            self._h, d, ptrs, c.tensor(lse, torch.float32, (d.rows,), "lse"),
-            c.tensor(loss_grad, torch.float32, (d.rows,), "loss_grad"), c.ranks(logit_grads, dt, shapes, "logit_grads"),
-            _stream(stream)), "hbmc_distill_loss_grad")
-
-    def _distill(self, c, logits, teacher_logits, teacher_ids, temperature):
-        first = _first(logits, "logits")
-        if first.dim() != 2 or teacher_logits.dim() != 2:
-            raise ValueError("logits are [rows, columns of the rank], teacher_logits [rows, top]")
-        n, top = teacher_logits.shape
-        if hasattr(logits, "data_ptr"):
-            vocab = logits.shape[0] * logits.shape[2]
-            shapes = (n, first.shape[1])
-        else:
-            vocab = sum([t.shape[1] for t in logits])
-            shapes = [(n, cols) for cols, _ in c.rows(vocab, 1)]
-        return (Distill(n, vocab, top, _float_type(first, "logits"), _float_type(teacher_logits, "teacher_logits"),
-                        _id_type(teacher_ids, "teacher_ids"), temperature,
-                        c.tensor(teacher_logits, teacher_logits.dtype, (n, top), "teacher_logits"),
-                        c.tensor(teacher_ids, teacher_ids.dtype, (n, top), "teacher_ids")),
-                c.ranks(logits, first.dtype, shapes, "logits"), first.dtype, shapes)
+        self._operate("distill_loss_grad", stream, logits, teacher_logits, teacher_ids, lse, loss_grad, logit_grads,
+                      temperature)
 
     def set_exec_mode(self, mode: str):
         """Launch form of every call: "auto" (default), "steps", "fused", "columns", "lds", "regs" or

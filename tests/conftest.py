@@ -25,6 +25,8 @@ def _ensure_built():
                    for f in os.listdir(os.path.join(ROOT, "allreduce_reduction_amd", "csrc")))
     if have_src and not os.path.exists(os.path.join(ROOT, "allreduce_reduction_amd", "libhbmcoll.so")):
         ge.build_hip()
+    if not os.path.exists(os.path.join(ROOT, "allreduce_reduction_amd", "_native.so")):
+        ge.build_binding()
 
 
 _ensure_built()

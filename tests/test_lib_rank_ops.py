@@ -224,41 +224,25 @@ def test_more_ranks_than_columns():
 # ------------------------------------------------------- the Python binding
 
 
-class Fake:
-    """The attributes that the binding reads of a device tensor."""
-
-    def __init__(self, shape, dtype=torch.bfloat16, addr=BASE, device=0, contiguous=True):
-        self.shape, self.dtype, self.addr, self.device_, self.contig = torch.Size(shape), dtype, addr, device, contiguous
-
-    def data_ptr(self):
-        return self.addr
-
-    def dim(self):
-        return len(self.shape)
-
-    def numel(self):
-        return self.shape.numel()
-
-    def get_device(self):
-        return self.device_
-
-    def is_contiguous(self):
-        return self.contig
-
-    def element_size(self):
-        return self.dtype.itemsize
-
-    def __len__(self):
-        return self.shape[0]
-
-
 @pytest.fixture()
 def on_device(monkeypatch):
-    monkeypatch.setattr(hc, "_current_device", lambda: 0)
+    """Host tensors stand in for device ones; calls that pass the checks must
+    not be made, except where the library itself refuses them."""
+    monkeypatch.setattr(hc, "_current_device", lambda: -1)
+    monkeypatch.setattr(hc, "_stream", lambda stream: 0)
+
+
+def one(shape, dtype=torch.bfloat16, contiguous=True):
+    if not contiguous:
+        return torch.zeros(shape[:-1] + (2 * shape[-1],), dtype=dtype)[..., ::2]
+    return torch.zeros(shape, dtype=dtype)
+
+
+Fake = one
 
 
 def fakes(n, shape, at=1, **kw):
-    return [Fake(shape, addr=BASE + ((at + r) << 20), **kw) for r in range(n)]
+    return [one(shape, **kw) for _ in range(n)]
 
 
 def norm_binding(c, **kw):
@@ -268,11 +252,11 @@ def norm_binding(c, **kw):
 
 
 @pytest.mark.parametrize("kw", [
-    dict(parts=fakes(3, (8, 16))), dict(parts=fakes(4, (8, 16), device=1)), dict(parts=fakes(4, (8, 16), contiguous=False)),
+    dict(parts=fakes(3, (8, 16))), dict(parts=fakes(4, (8, 16), contiguous=False)),
     dict(parts=fakes(4, (8, 16, 1))), dict(parts=[]), dict(residual=fakes(4, (8, 16), 10)),
     dict(residual=fakes(4, (2, 16), 10, dtype=torch.float16)), dict(out=fakes(4, (8, 15), 20)), dict(pre_weight=Fake((15,))),
-    dict(pre_weight=Fake((16,), torch.float32)), dict(gate=Fake((3, 16))), dict(gate=Fake((0, 16))), dict(gate=Fake((2, 8))),
-    dict(post_weight=Fake((16,), device=-1)), dict(sums=fakes(4, (8, 16), 30)), dict(residual_out=fakes(2, (2, 16), 30)),
+    dict(pre_weight=Fake((16,), torch.float32)), dict(gate=Fake((3, 16))), dict(gate=Fake((0, 16))), dict(gate=Fake((16,))), dict(gate=Fake((2, 8))),
+    dict(post_weight=Fake((16,), contiguous=False)), dict(sums=fakes(4, (8, 16), 30)), dict(residual_out=fakes(2, (2, 16), 30)),
 ])
 def test_norm_binding_refuses(comm, on_device, kw):
     with pytest.raises(ValueError):
@@ -283,21 +267,30 @@ def test_binding_types(comm, on_device):
     for dt in (torch.int32, torch.float64):
         with pytest.raises(TypeError):
             norm_binding(comm, parts=fakes(4, (8, 16), dtype=dt))
+    for bad in (3, "abcd", None, [1, 2, 3, 4], iter(())):
+        with pytest.raises(TypeError):
+            norm_binding(comm, parts=bad)
+    with pytest.raises(TypeError):
+        norm_binding(comm, scale="x")
+    with pytest.raises(ValueError):
+        norm_binding(comm, parts=Fake((3, 8, 16)))
     with pytest.raises(TypeError):  # one tensor cannot hold segments of unequal length
-        norm_binding(comm, residual=Fake((4, 2, 16)))
-    with pytest.raises(hc.HbmcError):  # out over the ranks' inputs in another order
-        norm_binding(comm, out=fakes(4, (8, 16))[::-1], stream=0)
+        norm_binding(comm, parts=fakes(4, (7, 16)), out=fakes(4, (7, 16)), residual=Fake((4, 2, 16)))
+    parts = fakes(4, (8, 16))
+    with pytest.raises(hc.HbmcError) as e:  # out over the ranks' inputs in another order
+        norm_binding(comm, parts=parts, out=parts[::-1])
+    assert e.value.code == BAD
 
 
 def test_norm_gradient_binding_refuses(comm, on_device):
     def call(**kw):
         a = dict(out_grads=fakes(4, (8, 16)), hidden=fakes(4, (2, 16), 10), part_grads=fakes(4, (8, 16), 20),
                  residual_grad=fakes(4, (2, 16), 30), pre_weight=Fake((16,)),
-                 pre_weight_grad=Fake((16,), torch.float32, BASE + (50 << 20)))
+                 pre_weight_grad=Fake((16,), torch.float32))
         a.update(kw)
         comm.reduce_norm_grad(*[a.pop(n) for n in ("out_grads", "hidden", "part_grads", "residual_grad", "pre_weight",
                                                    "pre_weight_grad")], **a)
-    w, wg = Fake((16,)), Fake((16,), torch.float32, BASE + (51 << 20))
+    w, wg = Fake((16,)), Fake((16,), torch.float32)
     for kw in (dict(post_weight=w), dict(post_weight_grad=wg), dict(post_weight=w, post_weight_grad=wg),
                dict(gate=Fake((1, 16))), dict(pre_weight_grad=Fake((16,))), dict(hidden=fakes(4, (3, 16), 10)),
                dict(residual_grad_in=fakes(4, (2, 15), 40)), dict(part_grads=fakes(4, (7, 16), 20))):
@@ -316,7 +309,7 @@ def test_embedding_binding_refuses(comm, on_device):
     for fn in ("embedding", "embedding_grad"):
         for kw in (dict(tables=fakes(4, (5,))), dict(tables=fakes(3, (5, 16)) + fakes(1, (6, 16), 5)), dict(tables=[]),
                    dict(ids=fakes(3, (3,), 10, dtype=torch.int64)), dict(ids=fakes(4, (3, 1), 10, dtype=torch.int64)),
-                   dict(out=fakes(4, (4, 16), 20)), dict(out=fakes(4, (3, 17), 20)), dict(out=fakes(4, (3, 16), 20, device=1))):
+                   dict(out=fakes(4, (4, 16), 20)), dict(out=fakes(4, (3, 17), 20))):
             with pytest.raises(ValueError):
                 call(fn, **kw)
         with pytest.raises(TypeError):
@@ -337,12 +330,11 @@ def test_distill_binding_refuses(comm, on_device):
         if fn == "loss":
             comm.distill_loss(a["logits"], a["t"], a["ids"], a["one"], a["two"], temperature=a["temperature"])
         else:
-            comm.distill_loss_grad(a["logits"], a["t"], a["ids"], a["one"], a["two"], a["grads"], temperature=a["temperature"],
-                                   stream=0)
+            comm.distill_loss_grad(a["logits"], a["t"], a["ids"], a["one"], a["two"], a["grads"], temperature=a["temperature"])
     for fn in ("loss", "grad"):
         for kw in (dict(logits=fakes(4, (4, 5))), dict(logits=fakes(3, (3, 5)) + fakes(1, (3, 6), 9)), dict(logits=fakes(4, (3,))),
                    dict(t=Fake((3,), f32)), dict(t=Fake((3, 3), f32)), dict(ids=Fake((4, 2), torch.int64)),
-                   dict(one=Fake((4,), f32)), dict(two=Fake((3,), torch.bfloat16)), dict(one=Fake((3,), f32, device=2))):
+                   dict(one=Fake((4,), f32)), dict(two=Fake((3,), torch.bfloat16)), dict(one=Fake((3,), f32, contiguous=False))):
             with pytest.raises(ValueError):
                 call(fn, **kw)
         for kw in (dict(t=Fake((3, 2), torch.int32)), dict(ids=Fake((3, 2), f32))):
@@ -354,12 +346,16 @@ def test_distill_binding_refuses(comm, on_device):
         call("grad", temperature=0.0)
 
 
-def test_host_tensors_never_reach_the_library(comm, on_device):
-    host = [torch.ones(8, 16) for _ in range(4)]
-    with pytest.raises(ValueError):
-        comm.reduce_norm(host, [t[:2] for t in host], host, torch.ones(16))
-    with pytest.raises(ValueError):
+def test_host_tensors_never_reach_the_library(comm, monkeypatch):
+    monkeypatch.setattr(hc, "_current_device", lambda: 0)
+    monkeypatch.setattr(hc, "_stream", lambda stream: 0)
+    host = fakes(4, (8, 16))
+    with pytest.raises(ValueError, match="on device 0 is needed"):
+        comm.reduce_norm(host, [t[:2] for t in host], host, torch.ones(16, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="on device 0 is needed"):
         comm.embedding(host, [torch.zeros(1, dtype=torch.int64)] * 4, [t[:1] for t in host])
+    with pytest.raises(ValueError, match="on device 0 is needed"):
+        comm.distill_loss(host, Fake((8, 2)), Fake((8, 2), torch.int64), Fake((8,), torch.float32), Fake((8,), torch.float32))
 
 
 # ------------------------------------------- the references' own gradients
