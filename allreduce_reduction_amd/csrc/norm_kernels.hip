@@ -12,18 +12,28 @@
 namespace hbmc {
 namespace dev {
 
-// A row is held by WAVES waves, VPT vectors of VE elements a lane; rows of one
-// or two waves share a workgroup of four.  Rows of 16 waves (kWide) have 128
+// A row is held by WAVES waves, VPT vectors of VE elements a lane.  Rows of 16 waves (kWide) have 128
 // registers a lane: they read weights, and in the gradient the row's own
 // operands, again where they are used (from L2) instead of holding them, and
 // keep two of the three weight gradients in LDS.
-template <int WAVES>
+// SLOTS rows share a workgroup.
+template <int WAVES, int SLOTS>
 struct RowTile {
   static constexpr int kThreads = 64 * WAVES;
-  static constexpr int kSlots = WAVES >= 4 ? 1 : 4 / WAVES;
+  static constexpr int kSlots = SLOTS;
   static constexpr int kGroup = kThreads * kSlots;
   static constexpr bool kWide = WAVES == 16;
 };
+
+template <int WAVES>
+using ForwardTile = RowTile<WAVES, (WAVES >= 4 ? 1 : 4 / WAVES)>;
+// The gradient's workgroups stay for many rows and leave one row of partial
+// sums each, so short rows share a workgroup of eight waves.  8 ranks, bf16, us
+// with 16, eight and four waves: 16384 rows of 512 81, 75 and 95; 8192 of 1024
+// 80, 77 and 96; 4096 of 2048 80, 78 and 95.
+constexpr int grad_slots(int waves) { return waves >= 8 ? 1 : 8 / waves; }
+template <int WAVES>
+using GradTile = RowTile<WAVES, grad_slots(WAVES)>;
 
 // Where a lane's k-th vector of a row starts.  The last vector of a row whose
 // width is no multiple of VE ends with the row, overlapping its neighbour by
@@ -38,7 +48,7 @@ struct Lane {
     const uint32_t n = (width + VE - 1) / VE;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const uint32_t v = tid + k * RowTile<WAVES>::kThreads;
+      const uint32_t v = tid + k * 64 * WAVES;
       on[k] = v < n;
       const uint32_t c = on[k] ? v : n - 1;  // idle lanes read what the last one reads
       at[k] = c * VE + VE > width ? width - VE : c * VE;
@@ -52,12 +62,12 @@ struct Lane {
 
 // Sums over a row's waves of N values that every wave holds; `turn` counts the
 // workgroup's calls, so that the buffer written is never one still being read.
-template <int WAVES, int N>
+template <int WAVES, int SLOTS, int N>
 __device__ __forceinline__ void row_sums(float (&x)[N], float* red, uint32_t slot, uint32_t wave, uint32_t* turn) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
   if constexpr (WAVES > 1) {
-    constexpr int kWidth = RowTile<WAVES>::kSlots * WAVES * 4;
+    constexpr int kWidth = SLOTS * WAVES * 4;
     float* mine = red + (*turn & 1) * kWidth + slot * WAVES * 4;
     ++*turn;
     if ((threadIdx.x & 63) == 0) {
@@ -126,6 +136,16 @@ __device__ __forceinline__ void sum_ranks(const unsigned char* const* bufs, int 
   }
 }
 
+// One vector to every rank, rank after rank: issued eight at a time the same
+// stores took 5% longer (8 ranks, 32 MiB each).
+template <typename K, bool NT>
+__device__ __forceinline__ void store_ranks(unsigned char* const* bufs, int P, uint64_t off, typename K::raw v) {
+  for (int p = 0; p < P; ++p) {
+    if constexpr (NT) K::store_nt(bufs[p] + off, v);
+    else K::store(bufs[p] + off, v);
+  }
+}
+
 // Sum of the terms f(i) of the lane's k-th vector that count for its row.
 template <int VE, typename L, typename F>
 __device__ __forceinline__ float vector_sum(const L& lane, int k, F&& f) {
@@ -140,10 +160,10 @@ __device__ __forceinline__ float vector_sum(const L& lane, int k, F&& f) {
   return lane.on[k] ? part : 0.0f;
 }
 
-template <int DT, int VE, int VPT, int WAVES>
-__global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_kernel(NormPtrs a, NormShape s) {
+template <int DT, int VE, int VPT, int WAVES, bool NT>
+__global__ __launch_bounds__(ForwardTile<WAVES>::kGroup) void norm_kernel(NormPtrs a, NormShape s) {
   typedef Pack<DT, VE> K;
-  typedef RowTile<WAVES> R;
+  typedef ForwardTile<WAVES> R;
   __shared__ float red[WAVES > 1 ? 2 * R::kSlots * WAVES * 4 : 1];
   const uint32_t wave_id = uniform(threadIdx.x >> 6);
   const uint32_t slot = wave_id / WAVES, wave = wave_id % WAVES;
@@ -181,7 +201,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_kernel(NormPtrs a
       float q[1] = {0.0f};
 #pragma unroll
       for (int k = 0; k < VPT; ++k) q[0] += vector_sum<VE>(lane, k, [&](int i) { return x[k][i] * x[k][i]; });
-      row_sums<WAVES>(q, red, slot, wave, &turn);
+      row_sums<WAVES, R::kSlots>(q, red, slot, wave, &turn);
       const float r1 = 1.0f / sqrtf(q[0] * inv + s.post_eps);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -209,7 +229,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_kernel(NormPtrs a
     float q[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < VPT; ++k) q[0] += vector_sum<VE>(lane, k, [&](int i) { return x[k][i] * x[k][i]; });
-    row_sums<WAVES>(q, red, slot, wave, &turn);
+    row_sums<WAVES, R::kSlots>(q, red, slot, wave, &turn);
     const float r2 = 1.0f / sqrtf(q[0] * inv + s.pre_eps);
     // every operand is in registers by now in every wave of the row, so the
     // outputs may lie where the operands lay
@@ -225,16 +245,16 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_kernel(NormPtrs a
 #pragma unroll
           for (int i = 0; i < VE; ++i) x[k][i] = x[k][i] * r2 * w[i];
           const typename K::raw y = K::narrow(x[k]);
-          for (int p = 0; p < s.P; ++p) K::store(a.out[p] + off + b, y);
+          store_ranks<K, NT>(a.out, s.P, off + b, y);
         }
     }
   }
 }
 
-template <int DT, int VE, int VPT, int WAVES>
-__global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormGradPtrs a, NormShape s) {
+template <int DT, int VE, int VPT, int WAVES, bool NT>
+__global__ __launch_bounds__(GradTile<WAVES>::kGroup) void norm_grad_kernel(NormGradPtrs a, NormShape s) {
   typedef Pack<DT, VE> K;
-  typedef RowTile<WAVES> R;
+  typedef GradTile<WAVES> R;
   __shared__ float red[WAVES > 1 ? 2 * R::kSlots * WAVES * 4 : 1];
   const uint32_t wave_id = uniform(threadIdx.x >> 6);
   const uint32_t slot = wave_id / WAVES, wave = wave_id % WAVES;
@@ -260,7 +280,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
 #pragma unroll
       for (int i = 0; i < VE; ++i) held[0][slot_of(k, i)] = held[1][slot_of(k, i)] = 0.0f;
   }
-  float* const mine = a.partial + uint64_t(chunk * R::kSlots + slot) * a.sets * s.width;
+  float* const mine = a.partial + uint64_t(a.direct ? chunk * R::kSlots + slot : chunk) * a.sets * s.width;
   if (a.direct && w1p) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
@@ -281,12 +301,11 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
       last = s.rows;
       flush = in + 1 == s.gate_rows && group * s.gate_rows < s.rows;
     } else {
+      // a gate group's rows dealt to its chunks in turn, so that the rows in
+      // work at one time lie side by side in memory
       const uint32_t g = chunk / a.chunks_per_group, first = g * s.gate_rows;
-      const uint32_t from = first + (chunk - g * a.chunks_per_group) * a.chunk_rows;
-      row = from + it * R::kSlots + slot;
-      last = from + a.chunk_rows;
-      if (last > first + s.gate_rows) last = first + s.gate_rows;
-      if (last > s.rows) last = s.rows;
+      row = first + (chunk - g * a.chunks_per_group + it * a.chunks_per_group) * R::kSlots + slot;
+      last = s.rows - first < s.gate_rows ? s.rows : first + s.gate_rows;
     }
     const bool active = row < last;
     row = uniform(active ? row : s.rows - 1);
@@ -331,7 +350,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
         q[2] += vector_sum<VE>(lane, k, [&](int i) { return x[i] * x[i]; });
       }
     }
-    row_sums<WAVES>(q, red, slot, wave, &turn);
+    row_sums<WAVES, R::kSlots>(q, red, slot, wave, &turn);
     const float r2 = 1.0f / sqrtf(q[0] * inv + s.pre_eps);
     const float c2 = r2 * r2 * r2 * (q[1] * inv);
     const float r1 = w1p ? 1.0f / sqrtf(q[2] * inv + s.post_eps) : 1.0f;
@@ -389,7 +408,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
       }
     }
     if (w1p) {
-      row_sums<WAVES>(inner, red, slot, wave, &turn);
+      row_sums<WAVES, R::kSlots>(inner, red, slot, wave, &turn);
       const float c1 = r1 * r1 * r1 * (inner[0] * inv);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -410,7 +429,7 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
       for (int k = 0; k < VPT; ++k)
         if (lane.on[k]) {
           const typename K::raw y = K::narrow(g[k]);
-          for (int p = 0; p < s.P; ++p) K::store(a.part_grads[p] + off + lane.at[k] * K::E, y);
+          store_ranks<K, NT>(a.part_grads, s.P, off + lane.at[k] * K::E, y);
         }
     }
     if (flush) {
@@ -444,6 +463,30 @@ __global__ __launch_bounds__(RowTile<WAVES>::kGroup) void norm_grad_kernel(NormG
 #pragma unroll
         for (int i = 0; i < VE; ++i) da[j][i] = 0.0f;
       }
+    }
+  }
+  if constexpr (R::kSlots > 1) {
+    if (!a.direct) {
+      // one row of partial sums for all slots, slots ascending
+      __shared__ float all[R::kGroup * VPT * VE];
+      const auto join = [&](float (&d)[D][VE]) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+          for (int i = 0; i < VE; ++i) all[(k * VE + i) * R::kGroup + threadIdx.x] = d[k][i];
+        __syncthreads();
+        if (slot == 0) {
+#pragma unroll
+          for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int i = 0; i < VE; ++i)
+              for (int w = 1; w < R::kSlots; ++w) d[k][i] += all[(k * VE + i) * R::kGroup + w * R::kThreads + threadIdx.x];
+        }
+      };
+      join(d2);
+      if (has_sum) join(da);
+      if (slot != 0) return;
     }
   }
 #pragma unroll
@@ -532,85 +575,107 @@ namespace {
 
 using namespace dev;
 
-// Vectors a lane and waves a row for a width, by row vectors n of 16 bytes
-// (or single elements below one vector).
+// Vectors a lane and waves a row, by row vectors n of 16 bytes (or single
+// elements below one vector).
 struct RowForm {
   int ve, vpt, waves;
 };
-RowForm row_form(int dtype, uint32_t width) {
+RowForm row_form(int dtype, uint32_t width, bool grad, uint32_t rows) {
   const int full = dtype == kF32 ? 4 : 8;
   if (width < static_cast<uint32_t>(full)) return {1, 1, 1};
   const uint32_t n = (width + full - 1) / full;
+  // Forward, two vectors a lane from 512 rows on.  8 ranks, bf16, two vectors
+  // and one: 8192 rows of 1024 60 and 66 us, 4096 of 2048 58.5 and 66, 4096 of
+  // 4096 111 and 115, 2048 of 8192 115 and 128; 256 rows of 4096 10.2 and 9.4.
+  // The gradient holds three times as much a lane and takes one, but for the
+  // widths above 512 vectors (2048 rows of 8192: 146 and 149 us).
+  const int two = !grad && rows >= 512 ? 2 : 1;
   if (n <= 64) return {full, 1, 1};
-  if (n <= 128) return {full, 1, 2};
-  if (n <= 256) return {full, 1, 4};
-  if (n <= 512) return {full, 1, 8};
-  if (n <= 1024) return {full, 1, 16};
+  if (n <= 128) return {full, two, 2 / two};
+  if (n <= 256) return {full, two, 4 / two};
+  if (n <= 512) return {full, two, 8 / two};
+  if (n <= 1024) return grad ? RowForm{full, 2, 8} : RowForm{full, two, 16 / two};
   if (n <= 2048) return {full, 2, 16};
   return {full, 4, 16};  // fp32 only: 16 elements a lane at most
 }
 
-template <typename F>
-hipError_t with_form(int dtype, uint32_t width, F&& f) {
-  const RowForm r = row_form(dtype, width);
-  const int key = r.vpt * 100 + r.waves;
-#define HBMC_FORMS(DT, VE)                                                                     \
-  switch (key) {                                                                               \
-    case 101: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 1>(), std::integral_constant<int, 1>());    \
-    case 102: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 1>(), std::integral_constant<int, 2>());    \
-    case 104: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 1>(), std::integral_constant<int, 4>());    \
-    case 108: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 1>(), std::integral_constant<int, 8>());    \
-    case 116: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 1>(), std::integral_constant<int, 16>());   \
-    case 216: return f(std::integral_constant<int, DT>(), std::integral_constant<int, VE>(),   \
-                       std::integral_constant<int, 2>(), std::integral_constant<int, 16>());   \
-    default: break;                                                                            \
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <int DT, int VE, bool GRAD, typename F>
+hipError_t with_waves(const RowForm& r, F&& f) {
+  const Int<DT> dt;
+  const Int<VE> ve;
+  switch (r.vpt * 100 + r.waves) {
+    case 101: return f(dt, ve, Int<1>(), Int<1>());
+    case 102: return f(dt, ve, Int<1>(), Int<2>());
+    case 104: return f(dt, ve, Int<1>(), Int<4>());
+    case 108: return f(dt, ve, Int<1>(), Int<8>());
+    case 208: return f(dt, ve, Int<2>(), Int<8>());
+    case 216: return f(dt, ve, Int<2>(), Int<16>());
+    default: break;
   }
-  if (r.ve == 1) {
-    const std::integral_constant<int, 1> one;
-    if (dtype == kF32) return f(std::integral_constant<int, kF32>(), one, one, one);
-    if (dtype == kF16) return f(std::integral_constant<int, kF16>(), one, one, one);
-    return f(std::integral_constant<int, kBF16>(), one, one, one);
+  if constexpr (!GRAD) {
+    switch (r.vpt * 100 + r.waves) {
+      case 201: return f(dt, ve, Int<2>(), Int<1>());
+      case 202: return f(dt, ve, Int<2>(), Int<2>());
+      case 204: return f(dt, ve, Int<2>(), Int<4>());
+      case 116: return f(dt, ve, Int<1>(), Int<16>());
+      default: break;
+    }
   }
-  if (dtype == kF32) {
-    HBMC_FORMS(kF32, 4)
-    return f(std::integral_constant<int, kF32>(), std::integral_constant<int, 4>(), std::integral_constant<int, 4>(),
-             std::integral_constant<int, 16>());
+  if constexpr (DT == kF32) {
+    if (r.vpt == 4) return f(dt, ve, Int<4>(), Int<16>());
   }
-  if (dtype == kF16) {
-    HBMC_FORMS(kF16, 8)
-  } else {
-    HBMC_FORMS(kBF16, 8)
-  }
-#undef HBMC_FORMS
   return hipErrorInvalidValue;
 }
 
-uint32_t slots_of(int waves) { return waves >= 4 ? 1 : 4 / waves; }
+template <bool GRAD, typename F>
+hipError_t with_form(int dtype, const RowForm& r, F&& f) {
+  if (r.ve == 1) {
+    const Int<1> one;
+    if (dtype == kF32) return f(Int<kF32>(), one, one, one);
+    if (dtype == kF16) return f(Int<kF16>(), one, one, one);
+    return f(Int<kBF16>(), one, one, one);
+  }
+  if (dtype == kF32) return with_waves<kF32, 4, GRAD>(r, f);
+  if (dtype == kF16) return with_waves<kF16, 8, GRAD>(r, f);
+  return with_waves<kBF16, 8, GRAD>(r, f);
+}
 
 constexpr uint32_t kMaxGrid = 1 << 20;  // workgroups of a launch; the kernel strides past it
 
 uint32_t up(uint32_t n, uint32_t by) { return n / by + (n % by != 0); }
 
+// Whether the ranks' copies are stored with the nontemporal hint: from 96 MiB
+// of them.  8 ranks, bf16, width 4096, with and without: 4096 rows (256 MiB)
+// 111 and 125 us, their gradient 139 and 150; 2048 rows 58 and 62, 79 and 86;
+// 1024 rows (64 MiB) 31 and 27, 47 and 47: there the cache takes the stores and
+// still holds them for whoever reads them next.
+bool stream_out(int dtype, const NormShape& s) {
+  return uint64_t(s.rows) * s.width * (dtype == kF32 ? 4 : 2) * s.P >= uint64_t(96) << 20;
+}
+
 }  // namespace
 
 hipError_t launch_norm(int dtype, const NormPtrs& a, const NormShape& s, hipStream_t stream) {
-  return with_form(dtype, s.width, [&](auto dt, auto ve, auto vpt, auto waves) {
-    constexpr uint32_t kSlots = RowTile<waves>::kSlots;
+  const bool nt = stream_out(dtype, s);
+  return with_form<false>(dtype, row_form(dtype, s.width, false, s.rows), [&](auto dt, auto ve, auto vpt, auto waves) {
+    constexpr uint32_t kSlots = ForwardTile<waves>::kSlots;
     void* argv[] = {const_cast<NormPtrs*>(&a), const_cast<NormShape*>(&s)};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&norm_kernel<dt, ve, vpt, waves>),
-                           dim3(std::min(up(s.rows, kSlots), kMaxGrid)), dim3(RowTile<waves>::kGroup), argv, 0, stream);
+    return hipLaunchKernel(nt ? reinterpret_cast<const void*>(&norm_kernel<dt, ve, vpt, waves, true>)
+                              : reinterpret_cast<const void*>(&norm_kernel<dt, ve, vpt, waves, false>),
+                           dim3(std::min(up(s.rows, kSlots), kMaxGrid)), dim3(ForwardTile<waves>::kGroup), argv, 0, stream);
   });
 }
 
 NormGradSplit split_norm_grad(int dtype, const NormShape& s) {
   NormGradSplit d;
-  const uint32_t S = d.slots = slots_of(row_form(dtype, s.width).waves);
-  const uint32_t target = 512;                                        // two workgroups a compute unit
+  const uint32_t S = grad_slots(row_form(dtype, s.width, true, s.rows).waves);
+  // One workgroup a compute unit: each more leaves a row of partial sums more
+  // (4096 rows of 4096, 8 ranks, bf16: 139 us with 256, 149 with 384, 144 with
+  // 512, 152 with 1024 workgroups, 190 with 128).
+  const uint32_t target = 256;
   const uint32_t C = up(std::max(up(s.rows, target), 1u), S) * S;  // rows a chunk
   const uint32_t R = s.gate_rows;
   d.groups = s.rows == 0 ? 0 : (s.rows - 1) / R + 1;
@@ -621,29 +686,31 @@ NormGradSplit split_norm_grad(int dtype, const NormShape& s) {
     d.iterations = d.groups_per_chunk / S * R;
   } else {
     d.chunks_per_group = up(R, C);
-    d.chunk_rows = up(R, d.chunks_per_group);
     d.chunks = d.groups * d.chunks_per_group;
-    d.iterations = up(d.chunk_rows, S);
+    d.iterations = up(R, d.chunks_per_group * S);
   }
   d.sets = s.post_weight || (s.gate && !d.direct) ? 2 : 1;
-  d.bytes = uint64_t(d.chunks) * S * d.sets * s.width * sizeof(float);
+  d.sums = d.direct ? d.chunks * S : d.chunks;
+  d.bytes = uint64_t(d.sums) * d.sets * s.width * sizeof(float);
   return d;
 }
 
 hipError_t launch_norm_grad(int dtype, NormGradPtrs& a, const NormShape& s, const NormGradSplit& d, float* pre_grad,
                             float* post_grad, float* gate_grad, hipStream_t stream) {
   a.gate_grad = gate_grad;
-  a.chunk_rows = d.chunk_rows;
   a.chunks_per_group = d.chunks_per_group;
   a.groups_per_chunk = d.groups_per_chunk;
   a.iterations = d.iterations;
   a.sets = d.sets;
   a.direct = d.direct;
   if (d.chunks > 0) {
-    const hipError_t e = with_form(dtype, s.width, [&](auto dt, auto ve, auto vpt, auto waves) {
+    const bool nt = stream_out(dtype, s);
+    const RowForm form = row_form(dtype, s.width, true, s.rows);
+    const hipError_t e = with_form<true>(dtype, form, [&](auto dt, auto ve, auto vpt, auto waves) {
       void* argv[] = {&a, const_cast<NormShape*>(&s)};
-      return hipLaunchKernel(reinterpret_cast<const void*>(&norm_grad_kernel<dt, ve, vpt, waves>),
-                             dim3(d.chunks), dim3(RowTile<waves>::kGroup), argv, 0, stream);
+      return hipLaunchKernel(nt ? reinterpret_cast<const void*>(&norm_grad_kernel<dt, ve, vpt, waves, true>)
+                                : reinterpret_cast<const void*>(&norm_grad_kernel<dt, ve, vpt, waves, false>),
+                             dim3(d.chunks), dim3(GradTile<waves>::kGroup), argv, 0, stream);
     });
     if (e != hipSuccess) return e;
   }
@@ -654,8 +721,8 @@ hipError_t launch_norm_grad(int dtype, NormGradPtrs& a, const NormShape& s, cons
   j.gate = gate_grad;
   j.gate_w = d.direct ? nullptr : static_cast<const unsigned char*>(s.gate);
   j.post_w = static_cast<const unsigned char*>(s.post_weight);
-  j.count = uint64_t(d.chunks) * d.slots;
-  j.per_group = std::max(d.chunks_per_group * d.slots, 1u);
+  j.count = d.sums;
+  j.per_group = std::max(d.chunks_per_group, 1u);
   j.sets = d.sets;
   j.width = s.width;
   const uint32_t jobs = 1 + (s.post_weight ? 1 : 0) + (s.gate && !d.direct ? d.groups : 0);

@@ -52,9 +52,9 @@ struct NormGradPtrs {
   unsigned char* residual_out[kMaxRanks];
   bool has_in;
   float* gate_grad;  // written here only when `direct`
-  float* partial;    // [chunks * slots][sets][width]
+  float* partial;    // [sums][sets][width]
   // A workgroup's chunk of rows (see split_norm_grad).
-  uint32_t chunk_rows, chunks_per_group, groups_per_chunk, iterations;
+  uint32_t chunks_per_group, groups_per_chunk, iterations;
   uint32_t sets;
   bool direct;
 };
@@ -62,8 +62,8 @@ struct NormGradPtrs {
 // Rows of the gradient kernel dealt to workgroups: the number of partial sums
 // and the workspace they need.
 struct NormGradSplit {
-  uint32_t chunks = 0, chunk_rows = 0, chunks_per_group = 0, groups_per_chunk = 0, iterations = 0, groups = 0;
-  uint32_t slots = 1, sets = 1;
+  uint32_t chunks = 0, chunks_per_group = 0, groups_per_chunk = 0, iterations = 0, groups = 0;
+  uint32_t sums = 0, sets = 1;  // rows of partial sums, kinds of sums in a row
   bool direct = false;
   uint64_t bytes = 0;
 };
@@ -154,6 +154,11 @@ struct Pack {
   }
   static __device__ __forceinline__ void store(unsigned char* p, raw v) {
     if constexpr (kVector) *reinterpret_cast<u32x4_any*>(p) = v;
+    else store_elem<E>(p, v);
+  }
+  // With the nontemporal hint, for outputs larger than the memory-side cache can hold.
+  static __device__ __forceinline__ void store_nt(unsigned char* p, raw v) {
+    if constexpr (kVector) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(p));
     else store_elem<E>(p, v);
   }
   static __device__ __forceinline__ void widen(raw v, float (&f)[VE]) {

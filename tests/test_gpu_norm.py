@@ -6,8 +6,8 @@ most 16 + 6 + 16 + 1 in each of the two row sums (a lane's terms, the wave, the
 waves, the mean), counted once for the value and half for the square root of
 each, and about 12 products: P + 16 + 39 + 12 < P + 80.  Gradient: two row sums
 one inside the other and up to 30 products: P + 2 * 39 + 30 < P + 120; the
-weights' gradients add the rows: at most 8 rows a chunk and 512 chunks by 16
-waves here, 8 + 32 + 16 more.
+weights' gradients add the rows: at most 9 rows a chunk and eight slots, 256
+chunks by 16 waves: 9 + 8 + 16 + 16 more, below 60.
 """
 import pytest
 import torch
@@ -101,6 +101,7 @@ SHAPES = [
     # widths, widths below a vector, more ranks than rows, one rank
     (8, 1, 4096), (4, 3, 512), (5, 7, 1001), (3, 5, 2049), (2, 9, 7), (1, 4, 1), (16, 2, 130), (64, 3, 72),
     (8, 65, 256), (7, 33, 1024), (2, 3, 8192), (3, 2, 16384), (9, 2, 16383), (2, 5, 8193), (12, 700, 64), (1, 600, 40),
+    (2, 513, 1000), (2, 512, 1999), (2, 520, 4095), (1, 512, 8190),
 ]
 
 
@@ -130,6 +131,14 @@ def test_variants(post, T, H, gates):
     with hc.Comm(3, "rhd") as comm:
         check_forward(forward(c, comm, save=gates != 2), c, save=gates != 2)
         check_backward(*backward(c, comm, has_in=gates != 1))
+
+
+def test_stores_past_the_cache():
+    """96 MiB of outputs and more are stored past the caches."""
+    c = case(4, 2049, 6400, "bf16", True, 3)
+    with hc.Comm(4, "ring") as comm:
+        check_forward(forward(c, comm), c)
+        check_backward(*backward(c, comm))
 
 
 @pytest.mark.parametrize("H", [64, 1001])
