@@ -86,14 +86,36 @@ struct SortArgs {
   const unsigned char* ids[kMaxRanks];
   uint32_t tokens[kMaxRanks];
   int P, id_bytes;
-  uint32_t vocab, total, tile, tiles, bits, passes;
-  uint32_t* hist;     // [passes][tiles][kMaxBins]
+  uint32_t vocab, total, tiles, bits, passes;
+  uint32_t* hist;     // [tiles][kMaxBins], of the pass at work
   uint32_t* key[2];   // sorted so far, and place beside it
   uint32_t* place[2];
-  uint32_t* touched;  // a bit for each id that occurs, or nullptr
+  unsigned char* touched;  // 1 for each id that occurs, or nullptr
+  // the table's gradient cleared by the workgroups past the tiles (nullptr: not)
+  unsigned char* clear[kMaxRanks];
+  uint64_t clear_bytes[kMaxRanks];
+  uint32_t clear_units, clear_first;  // units of kClearUnit bytes a rank; the first of this launch
 };
 
-// Ranks' first tokens among all ranks' (before[P] = total) in LDS.
+constexpr uint32_t kClearUnit = 1024 * 16 * 8;
+
+// The unit-th piece of the ranks' gradients set to zero.
+__device__ __forceinline__ void clear_piece(const SortArgs& a, uint32_t unit) {
+  const uint32_t rank = unit / a.clear_units;
+  const uint64_t from = uint64_t(unit - rank * a.clear_units) * kClearUnit, end = a.clear_bytes[rank];
+  unsigned char* to = a.clear[rank];
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) {
+    const uint64_t at = from + (k * 1024 + threadIdx.x) * 16;
+    if (at + 16 <= end) {
+      *reinterpret_cast<u32x4_any*>(to + at) = u32x4{};
+    } else {
+      for (uint64_t b = at; b < end; b += 2) *reinterpret_cast<uint16_t*>(to + b) = 0;  // whole elements of 2 or 4 bytes
+    }
+  }
+}
+
+// Ranks' first tokens among all ranks' in LDS.
 __device__ __forceinline__ void rank_starts(const SortArgs& a, uint32_t* before) {
   if (threadIdx.x < 64) {
     uint32_t x = static_cast<int>(threadIdx.x) < a.P ? a.tokens[threadIdx.x] : 0;
@@ -120,34 +142,31 @@ __device__ __forceinline__ uint32_t token_key(const SortArgs& a, const uint32_t*
   return id >= 0 && id < static_cast<int64_t>(a.vocab) ? static_cast<uint32_t>(id) : a.vocab;
 }
 
-__device__ __forceinline__ void read_pair(const SortArgs& a, const uint32_t* before, uint32_t pass, uint32_t i,
-                                          uint32_t* key, uint32_t* place) {
-  if (pass == 0) {
-    *key = token_key(a, before, i, place);
-  } else {
-    *key = a.key[(pass + 1) & 1][i];
-    *place = a.place[(pass + 1) & 1][i];
-  }
-}
-
-// First pass over the ids: the first digit's counts in each tile; clears the
-// later digits' counts and the touched bits.
-__global__ __launch_bounds__(1024) void embed_count_kernel(SortArgs a) {
+// A tile's counts of the pass's digit; before the first pass also clears
+// `touched`.  R: pairs a thread.
+template <int R>
+__global__ __launch_bounds__(1024) void embed_count_kernel(SortArgs a, uint32_t pass) {
   __shared__ uint32_t before[64], bins[kMaxBins];
-  const uint32_t n = 1u << a.bits;
-  rank_starts(a, before);
+  if (blockIdx.x >= a.tiles) {
+    clear_piece(a, a.clear_first + blockIdx.x - a.tiles);
+    return;
+  }
+  const uint32_t shift = pass * a.bits, mask = (1u << a.bits) - 1;
   bins[threadIdx.x] = 0;
-  __syncthreads();
-  const uint32_t lo = blockIdx.x * a.tile, hi = min(lo + a.tile, a.total);
-  for (uint32_t i = lo + threadIdx.x; i < hi; i += 1024) {
+  if (pass == 0) rank_starts(a, before);
+  else __syncthreads();
+  const uint32_t lo = blockIdx.x * R * 1024;
+#pragma unroll
+  for (uint32_t r = 0; r < R; ++r) {
+    const uint32_t i = lo + r * 1024 + threadIdx.x;
     uint32_t place;
-    atomicAdd(&bins[token_key(a, before, i, &place) & (n - 1)], 1u);
+    if (i < a.total) atomicAdd(&bins[(pass == 0 ? token_key(a, before, i, &place) : a.key[(pass + 1) & 1][i]) >> shift & mask], 1u);
   }
   __syncthreads();
   a.hist[blockIdx.x * kMaxBins + threadIdx.x] = bins[threadIdx.x];
-  for (uint32_t p = 1; p < a.passes; ++p) a.hist[(p * a.tiles + blockIdx.x) * kMaxBins + threadIdx.x] = 0;
-  if (a.touched)
-    for (uint32_t w = blockIdx.x * 1024 + threadIdx.x; w < (a.vocab + 31) / 32; w += gridDim.x * 1024) a.touched[w] = 0;
+  if (a.touched && pass == 0)
+    for (uint32_t w = blockIdx.x * 1024 + threadIdx.x; w < (a.vocab + 3) / 4; w += a.tiles * 1024)
+      reinterpret_cast<uint32_t*>(a.touched)[w] = 0;
 }
 
 // Lanes of the wave whose digit equals this lane's (`on` lanes only).
@@ -166,109 +185,160 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// One stable pass over a tile's pairs.  Every wave counts its own stretch of
-// the tile by digit, the counts become each wave's first positions, and the
-// wave places its pairs in order.
-template <bool SINGLE>
-__device__ __forceinline__ void sort_pass(const SortArgs& a, const uint32_t* before, uint32_t pass, uint32_t (*count)[kMaxBins],
-                                          uint32_t* scan) {
+// Where a tile's pairs go: each wave ranks its own stretch of 64 * R pairs by
+// digit, counting in LDS as it goes, and the waves' counts and the tiles'
+// (`all` and `prior`: of bin threadIdx.x in all tiles, in those before this
+// one) become each wave's first positions.  to[r]: the r-th pair's position.
+template <int R, typename Counts>
+__device__ __forceinline__ void sort_positions(const uint32_t (&key)[R], const bool (&on)[R], uint32_t shift, uint32_t bits,
+                                               uint32_t (*count)[kMaxBins], uint32_t* scan, Counts&& counts, uint32_t (&to)[R]) {
   const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const uint32_t tile = SINGLE ? 0 : blockIdx.x;
-  const uint32_t shift = pass * a.bits, mask = (1u << a.bits) - 1;
-  const bool last = pass + 1 == a.passes;
-  const uint32_t stretch = a.tile / kSortWaves;
-  const uint32_t lo = tile * a.tile + wave * stretch;
+  const uint32_t mask = (1u << bits) - 1;
   const uint64_t below = (uint64_t(1) << lane) - 1;
 #pragma unroll
   for (uint32_t w = 0; w < kSortWaves; ++w) count[w][threadIdx.x] = 0;
   __syncthreads();
-  for (uint32_t r = 0; r < stretch && lo + r < a.total; r += 64) {
-    const uint32_t i = lo + r + lane;
-    const bool on = i < a.total;
-    uint32_t key = 0, place;
-    if (on) read_pair(a, before, pass, i, &key, &place);
-    const uint32_t digit = key >> shift & mask;
-    const uint64_t same = same_digit(digit, a.bits, on);
-    if (on && (same & below) == 0) count[wave][digit] += __popcll(same);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t digit = key[r] >> shift & mask;
+    const uint64_t same = same_digit(digit, bits, on[r]);
+    to[r] = 0;
+    if (on[r]) to[r] = count[wave][digit] + __popcll(same & below);
     wave_order();
-    // a frequent id's bit is mostly there already (an old value read only costs the atomic)
-    if (pass == 0 && a.touched && on && key < a.vocab && !(a.touched[key >> 5] >> (key & 31) & 1))
-      atomicOr(&a.touched[key >> 5], 1u << (key & 31));
+    if (on[r] && (same & below) == 0) count[wave][digit] += __popcll(same);
+    wave_order();
   }
   __syncthreads();
-  {
-    // bin threadIdx.x: pairs in all tiles, and in the tiles before this one
-    uint32_t all = 0, prior = 0;
-    if constexpr (SINGLE) {
+  uint32_t all, prior;
+  counts(&all, &prior);
+  uint32_t x = all;
 #pragma unroll
-      for (uint32_t w = 0; w < kSortWaves; ++w) all += count[w][threadIdx.x];
-    } else {
-      const uint32_t* h = a.hist + uint64_t(pass) * a.tiles * kMaxBins + threadIdx.x;
-#pragma unroll 8
-      for (uint32_t t = 0; t < a.tiles; ++t) {
-        const uint32_t c = h[t * kMaxBins];
-        all += c;
-        prior += t < tile ? c : 0;
-      }
-    }
-    uint32_t x = all;
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(x, d);
+    if (static_cast<int>(lane) >= d) x += y;
+  }
+  if (lane == 63) scan[wave] = x;
+  __syncthreads();
+  uint32_t first = x - all + prior;
+  for (uint32_t w = 0; w < wave; ++w) first += scan[w];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const uint32_t y = __shfl_up(x, d);
-      if (static_cast<int>(lane) >= d) x += y;
-    }
-    if (lane == 63) scan[wave] = x;
-    __syncthreads();
-    uint32_t first = x - all + prior;
-    for (uint32_t w = 0; w < wave; ++w) first += scan[w];
-#pragma unroll
-    for (uint32_t w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = count[w][threadIdx.x];
-      count[w][threadIdx.x] = first;
-      first += c;
-    }
+  for (uint32_t w = 0; w < kSortWaves; ++w) {
+    const uint32_t c = count[w][threadIdx.x];
+    count[w][threadIdx.x] = first;
+    first += c;
   }
   __syncthreads();
-  uint32_t* next = last ? nullptr : a.hist + uint64_t(pass + 1) * a.tiles * kMaxBins;
-  for (uint32_t r = 0; r < stretch && lo + r < a.total; r += 64) {
-    const uint32_t i = lo + r + lane;
-    const bool on = i < a.total;
-    uint32_t key = 0, place = 0;
-    if (on) read_pair(a, before, pass, i, &key, &place);
-    const uint32_t digit = key >> shift & mask;
-    const uint64_t same = same_digit(digit, a.bits, on);
-    const uint32_t to = on ? count[wave][digit] + __popcll(same & below) : 0;
-    wave_order();
-    if (on && (same & below) == 0) count[wave][digit] += __popcll(same);
-    wave_order();
-    if (on) {
-      a.key[pass & 1][to] = key;
-      a.place[pass & 1][to] = place;
-      if constexpr (!SINGLE) {
-        if (next) atomicAdd(&next[to / a.tile * kMaxBins + (key >> (shift + a.bits) & mask)], 1u);
-      }
-    }
-  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (on[r]) to[r] += count[wave][key[r] >> shift & mask];
 }
 
+// Marks the ids that occur, a byte each: stores of one value need no order
+// (bits set by atomics took 85 us for 32768 tokens, a third of them in one word).
+template <int R>
+__device__ __forceinline__ void mark(const SortArgs& a, const uint32_t (&key)[R], const bool (&on)[R]) {
+  if (!a.touched) return;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (on[r] && key[r] < a.vocab) a.touched[key[r]] = 1;
+}
+
+template <int R>
 __global__ __launch_bounds__(1024) void embed_sort_kernel(SortArgs a, uint32_t pass) {
   __shared__ uint32_t before[64], scan[kSortWaves], count[kSortWaves][kMaxBins];
-  rank_starts(a, before);
-  sort_pass<false>(a, before, pass, count, scan);
+  if (blockIdx.x >= a.tiles) {
+    clear_piece(a, a.clear_first + blockIdx.x - a.tiles);
+    return;
+  }
+  if (pass == 0) rank_starts(a, before);
+  const uint32_t lo = blockIdx.x * R * 1024 + uniform(threadIdx.x >> 6) * R * 64 + (threadIdx.x & 63);
+  uint32_t key[R], place[R], to[R];
+  bool on[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t i = lo + r * 64;
+    on[r] = i < a.total;
+    key[r] = place[r] = 0;
+    if (on[r]) {
+      if (pass == 0) {
+        key[r] = token_key(a, before, i, &place[r]);
+      } else {
+        key[r] = a.key[(pass + 1) & 1][i];
+        place[r] = a.place[(pass + 1) & 1][i];
+      }
+    }
+  }
+  // the tiles' counts, on their way while the pairs are ranked
+  uint32_t all = 0, prior = 0;
+  const uint32_t* h = a.hist + threadIdx.x;
+#pragma unroll 16
+  for (uint32_t t = 0; t < a.tiles; ++t) {
+    const uint32_t c = h[t * kMaxBins];
+    all += c;
+    prior += t < blockIdx.x ? c : 0;
+  }
+  sort_positions<R>(key, on, pass * a.bits, a.bits, count, scan, [&](uint32_t* x, uint32_t* y) { *x = all, *y = prior; }, to);
+  if (pass == 0) mark<R>(a, key, on);
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (on[r]) {
+      a.key[pass & 1][to[r]] = key[r];
+      a.place[pass & 1][to[r]] = place[r];
+    }
 }
 
-// All passes of a call whose pairs are one tile.
+// All passes of a call whose pairs are one tile, between them in LDS.
+template <int R>
 __global__ __launch_bounds__(1024) void embed_sort_all_kernel(SortArgs a) {
   __shared__ uint32_t before[64], scan[kSortWaves], count[kSortWaves][kMaxBins];
+  __shared__ uint2 pairs[R * 1024];
+  if (blockIdx.x >= 1) {
+    clear_piece(a, a.clear_first + blockIdx.x - 1);
+    return;
+  }
   rank_starts(a, before);
-  if (a.touched)
-    for (uint32_t w = threadIdx.x; w < (a.vocab + 31) / 32; w += 1024) a.touched[w] = 0;
-  for (uint32_t pass = 0; pass < a.passes; ++pass) {
-    // the pairs of the last pass, and the cleared bits, before this one
+  if (a.touched) {
+    for (uint32_t w = threadIdx.x; w < (a.vocab + 3) / 4; w += 1024) reinterpret_cast<uint32_t*>(a.touched)[w] = 0;
     __threadfence();
     __syncthreads();
-    sort_pass<true>(a, before, pass, count, scan);
   }
+  const uint32_t lo = uniform(threadIdx.x >> 6) * R * 64 + (threadIdx.x & 63);
+  uint32_t key[R], place[R], to[R];
+  bool on[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    on[r] = lo + r * 64 < a.total;
+    key[r] = place[r] = 0;
+    if (on[r]) key[r] = token_key(a, before, lo + r * 64, &place[r]);
+  }
+  mark<R>(a, key, on);
+  for (uint32_t pass = 0; pass < a.passes; ++pass) {
+    sort_positions<R>(key, on, pass * a.bits, a.bits, count, scan, [&](uint32_t* all, uint32_t* prior) {
+      *all = *prior = 0;
+#pragma unroll
+      for (uint32_t w = 0; w < kSortWaves; ++w) *all += count[w][threadIdx.x];
+    }, to);
+    if (pass + 1 == a.passes) break;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (on[r]) pairs[to[r]] = uint2{key[r], place[r]};
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (on[r]) {
+        const uint2 p = pairs[lo + r * 64];
+        key[r] = p.x;
+        place[r] = p.y;
+      }
+    // the next pass's first barrier is behind its counts alone: pairs are
+    // written again only after its later ones
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    if (on[r]) {
+      a.key[0][to[r]] = key[r];
+      a.place[0][to[r]] = place[r];
+    }
 }
 
 // ---------------------------------------------------------------- the sums
@@ -280,58 +350,67 @@ struct SumArgs {
   float scale;
   const uint32_t* key;
   const uint32_t* place;
-  const uint32_t* touched;  // nullptr: add to the rows that occur, leave the others
+  const unsigned char* touched;  // the rows that occur, for those that clear the others
+  bool accumulate;
   float* partial;           // [chunks][2][width]: of a chunk's first id, of its last
   uint32_t sum_groups;      // workgroups that add; those after them clear rows
   uint32_t clear_rows;      // rows a wave clears
 };
 
-// The finished sum of id `key`, at the lane's columns.
-template <int DT, int GT, int VE>
-__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, const Column<VE>& c, float (&acc)[VE]) {
-  constexpr uint32_t G = Width<GT>::bytes;
+// Where the lane's columns of id `key` lie in the gradient, and what is there.
+template <int GT>
+__device__ __forceinline__ unsigned char* grad_at(const SumArgs& a, uint32_t key, uint32_t at) {
   const uint32_t owner = key / a.seg;
-  unsigned char* to = a.out[owner] + (uint64_t(key - owner * a.seg) * a.width + c.at) * G;
-  if (!c.on) return;
+  return a.out[owner] + (uint64_t(key - owner * a.seg) * a.width + at) * Width<GT>::bytes;
+}
+template <int GT, int VE>
+__device__ __forceinline__ void load_row(const unsigned char* p, float (&f)[VE]) {
+  if constexpr (VE * Width<GT>::bytes <= 16) {
+    Pack<GT, VE>::widen(Pack<GT, VE>::load(p), f);
+  } else {
 #pragma unroll
-  for (int i = 0; i < VE; ++i) acc[i] *= a.scale;
-  if (a.touched == nullptr) {
-    if (c.dup != 0) {
+    for (int i = 0; i < VE; i += 4) {
+      const f32x4_any v = *reinterpret_cast<const f32x4_any*>(p + i * 4);
+      f[i] = v.x, f[i + 1] = v.y, f[i + 2] = v.z, f[i + 3] = v.w;
+    }
+  }
+}
+
+// The finished sum of id `key` (scaled, and added to `old` where the call
+// accumulates), at the lane's columns.
+template <int GT, int VE>
+__device__ __forceinline__ void write_row(const SumArgs& a, uint32_t key, const Column<VE>& c, float (&acc)[VE],
+                                          const float (&old)[VE]) {
+  if (!c.on) return;
+  unsigned char* to = grad_at<GT>(a, key, c.at);
+#pragma unroll
+  for (int i = 0; i < VE; ++i) acc[i] = a.accumulate ? old[i] + acc[i] * a.scale : acc[i] * a.scale;
+  if constexpr (VE > 1) {
+    if (a.accumulate && c.dup != 0) {
       // a row's last two lanes share columns; only one of them may add
 #pragma unroll
       for (int i = 0; i < VE; ++i) {
-        if (i < static_cast<int>(c.dup)) continue;
-        float old[1];
-        Pack<GT, 1>::widen(Pack<GT, 1>::load(to + i * G), old);
-        old[0] += acc[i];
-        Pack<GT, 1>::store(to + i * G, Pack<GT, 1>::narrow(old));
+        const float one[1] = {acc[i]};
+        if (i >= static_cast<int>(c.dup)) Pack<GT, 1>::store(to + i * Width<GT>::bytes, Pack<GT, 1>::narrow(one));
       }
       return;
     }
-    float old[VE];
-    if constexpr (GT == DT) {
-      Pack<GT, VE>::widen(Pack<GT, VE>::load(to), old);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VE; ++i) old[i] = reinterpret_cast<const float*>(to)[i];
-    }
-#pragma unroll
-    for (int i = 0; i < VE; ++i) acc[i] += old[i];
   }
-  if constexpr (GT == DT) Pack<GT, VE>::store(to, Pack<GT, VE>::narrow(acc));
+  if constexpr (VE * Width<GT>::bytes <= 16) Pack<GT, VE>::store(to, Pack<GT, VE>::narrow(acc));
   else store_floats<VE>(reinterpret_cast<float*>(to), acc);
 }
 
 template <int DT, int GT, int VE>
 __global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
   typedef Pack<DT, VE> K;
+  constexpr uint32_t U = 8;  // tokens whose loads are in flight
   const uint32_t lane = threadIdx.x & 63;
   if (blockIdx.x >= a.sum_groups) {
     constexpr int GE = VE == 1 ? 1 : 16 / Width<GT>::bytes;
     typedef Pack<GT, GE> Z;
     const uint32_t first = ((blockIdx.x - a.sum_groups) * 4 + uniform(threadIdx.x >> 6)) * a.clear_rows;
     for (uint32_t r = first; r < first + a.clear_rows && r < a.vocab; ++r) {
-      if (a.touched[r >> 5] >> (r & 31) & 1) continue;
+      if (a.touched[r]) continue;
       const uint32_t owner = r / a.seg;
       unsigned char* to = a.out[owner] + uint64_t(r - owner * a.seg) * a.width * Z::E;
       for (uint32_t v = lane; v * GE < a.width; v += 64) {
@@ -347,92 +426,108 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(SumArgs a) {
   if (chunk >= a.chunks) return;
   const Column<VE> c(static_cast<uint32_t>(unit - uint64_t(chunk) * pieces) * 64 + lane, a.width);
   const uint32_t lo = chunk * a.chunk, hi = min(lo + a.chunk, a.total);
-  uint32_t cur = uniform(a.key[lo]);
-  if (cur >= a.vocab) return;  // tokens without a row come last
-  bool shared = lo > 0 && uniform(a.key[lo > 0 ? lo - 1 : 0]) == cur;  // the current id began in an earlier chunk
-  const uint32_t after = hi < a.total ? uniform(a.key[hi]) : a.vocab;
+  const uint32_t keys = lo + lane < hi ? a.key[lo + lane] : a.vocab;
+  const uint32_t places = lo + lane < hi ? a.place[lo + lane] : 0;
+  const uint32_t n = __popcll(__ballot(keys < a.vocab));  // tokens without a row come last
+  if (n == 0) return;
+  const auto key_of = [&](uint32_t t) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(keys), t)); };
+  const uint32_t begun = lo > 0 ? uniform(a.key[lo - 1]) : a.vocab;     // the id that began in an earlier chunk
+  const uint32_t after = hi < a.total ? uniform(a.key[hi]) : a.vocab;  // the id that a later chunk begins with
   float* partial = a.partial + uint64_t(chunk) * 2 * a.width + c.at;
   float acc[VE] = {};
-  const auto finish = [&](bool goes_on) {
-    if (!shared && !goes_on) write_row<DT, GT, VE>(a, cur, c, acc);
-    else if (c.on) store_floats<VE>(partial + (shared ? 0 : a.width), acc);
-  };
-  for (uint32_t base = lo; base < hi; base += 64) {
-    const uint32_t i = base + lane;
-    const uint32_t keys = i < hi ? a.key[i] : a.vocab;
-    const uint32_t places = i < hi ? a.place[i] : 0;
-    const uint32_t n = __popcll(__ballot(keys < a.vocab));  // sorted: the first n lanes
-    for (uint32_t t = 0; t < n; t += 8) {
-      typename K::raw v[8];
+  for (uint32_t t = 0; t < n; t += U) {
+    typename K::raw v[U];
+    float old[U][VE] = {};
 #pragma unroll
-      for (uint32_t u = 0; u < 8; ++u) {
-        const uint32_t pl = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(places), min(t + u, n - 1)));
-        const unsigned char* row = a.rows[pl >> kPlaceBits] + uint64_t(pl & ((1u << kPlaceBits) - 1)) * a.width * K::E;
-        v[u] = K::stream(row + c.at * K::E);
-      }
+    for (uint32_t u = 0; u < U; ++u) {
+      const uint32_t at = min(t + u, n - 1);
+      const uint32_t pl = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(places), at));
+      const unsigned char* row = a.rows[pl >> kPlaceBits] + uint64_t(pl & ((1u << kPlaceBits) - 1)) * a.width * K::E;
+      v[u] = K::stream(row + c.at * K::E);
+    }
+    if (a.accumulate) {
+      // what the rows finished here hold, on its way with their tokens
 #pragma unroll
-      for (uint32_t u = 0; u < 8; ++u) {
-        if (t + u < n) {
-          const uint32_t key = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(keys), t + u));
-          if (key != cur) {
-            finish(false);
-#pragma unroll
-            for (int i2 = 0; i2 < VE; ++i2) acc[i2] = 0.0f;
-            cur = key;
-            shared = false;
-          }
-          float f[VE];
-          K::widen(v[u], f);
-#pragma unroll
-          for (int i2 = 0; i2 < VE; ++i2) acc[i2] += f[i2];
-        }
+      for (uint32_t u = 0; u < U; ++u) {
+        if (t + u >= n) continue;
+        const uint32_t key = key_of(t + u), next = t + u + 1 < n ? key_of(t + u + 1) : after;
+        if (key != next && key != begun) load_row<GT, VE>(grad_at<GT>(a, key, c.at), old[u]);
       }
     }
-    if (n < 64) break;
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      if (t + u >= n) continue;
+      float f[VE];
+      K::widen(v[u], f);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) acc[i] += f[i];
+      const uint32_t key = key_of(t + u), next = t + u + 1 < n ? key_of(t + u + 1) : after;
+      if (key != next || t + u + 1 == n) {
+        // the id's last token here: finished, or left for joining
+        if (key != begun && key != next) write_row<GT, VE>(a, key, c, acc, old[u]);
+        else if (c.on) store_floats<VE>(partial + (key == begun ? 0 : a.width), acc);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[i] = 0.0f;
+      }
+    }
   }
-  finish(after == cur);
 }
 
-// Joins the sums of an id that spans chunks: by the chunk it begins in.
+// Joins the sums of an id that spans chunks: a workgroup for each piece of a row
+// and the chunk the id begins in (most find nothing to join), its four waves
+// taking a quarter of the later chunks each.  One workgroup a chunk, for all of
+// a row's pieces, took twice as long: a frequent id is then one compute unit's.
 template <int DT, int GT, int VE>
 __global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
-  const uint32_t lane = threadIdx.x & 63;
+  __shared__ float parts[4][VE][64];
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t pieces = (a.width + VE * 64 - 1) / (VE * 64);
-  const uint64_t unit = uint64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6);
-  const uint32_t chunk = static_cast<uint32_t>(unit / pieces);
-  if (chunk + 1 >= a.chunks) return;
+  const uint32_t chunk = blockIdx.x / pieces;
   const uint32_t lo = chunk * a.chunk, hi = lo + a.chunk;
-  const uint32_t key = uniform(a.key[hi - 1]);
-  if (key >= a.vocab || uniform(a.key[hi]) != key) return;                              // ends here
-  if (lo > 0 && uniform(a.key[lo]) == key && uniform(a.key[lo - 1]) == key) return;     // began earlier
-  const Column<VE> c(static_cast<uint32_t>(unit - uint64_t(chunk) * pieces) * 64 + lane, a.width);
-  const float* head = a.partial + c.at;
+  const uint32_t key = uniform(a.key[hi - 1]), next = uniform(a.key[hi]);
+  const uint32_t first = uniform(a.key[lo]), before = lo > 0 ? uniform(a.key[lo - 1]) : a.vocab;
+  if (key >= a.vocab || next != key || (first == key && before == key)) return;  // ends here, or began earlier
+  const Column<VE> c((blockIdx.x - chunk * pieces) * 64 + lane, a.width);
   const uint64_t step = uint64_t(2) * a.width;
-  float acc[VE];
-#pragma unroll
-  for (int i = 0; i < VE; ++i) acc[i] = head[chunk * step + a.width + i];
-  for (uint32_t next = chunk + 1; next < a.chunks; next += 64) {
-    const uint32_t mine = next + lane;
+  const float* head = a.partial + (chunk + 1) * step + c.at;
+  uint32_t n = 0;  // later chunks that begin with the id
+  for (uint32_t from = chunk + 1; from < a.chunks; from += 64) {
+    const uint32_t mine = from + lane;
     const bool same = mine < a.chunks && a.key[uint64_t(mine) * a.chunk] == key;
-    const uint32_t n = __popcll(__ballot(same));  // sorted: the first n of them
-    uint32_t t = 0;
-    for (; t + 4 <= n; t += 4) {
-      float f[4][VE];
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) f[u][i] = head[(next + t + u) * step + i];
-#pragma unroll
-      for (uint32_t u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) acc[i] += f[u][i];
-    }
-    for (; t < n; ++t)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) acc[i] += head[(next + t) * step + i];
-    if (n < 64) break;
+    const uint32_t more = __popcll(__ballot(same));  // sorted: the first of them
+    n += more;
+    if (more < 64) break;
   }
-  write_row<DT, GT, VE>(a, key, c, acc);
+  const uint32_t each = (n + 3) / 4, end = min(n, (wave + 1) * each);
+  float acc[VE] = {};
+  uint32_t t = wave * each;
+  for (; t + 4 <= end; t += 4) {
+    float f[4][VE];
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u) load_row<kF32, VE>(reinterpret_cast<const unsigned char*>(head + (t + u) * step), f[u]);
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) acc[i] += f[u][i];
+  }
+  for (; t < end; ++t) {
+    float f[VE];
+    load_row<kF32, VE>(reinterpret_cast<const unsigned char*>(head + t * step), f);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) acc[i] += f[i];
+  }
+#pragma unroll
+  for (int i = 0; i < VE; ++i) parts[wave][i][lane] = acc[i];
+  __syncthreads();
+  if (wave != 0) return;
+  float old[VE] = {};
+  if (a.accumulate) load_row<GT, VE>(grad_at<GT>(a, key, c.at), old);
+  load_row<kF32, VE>(reinterpret_cast<const unsigned char*>(head - step + a.width), acc);  // the id's beginning
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) acc[i] += parts[w][i][lane];
+  write_row<GT, VE>(a, key, c, acc, old);
 }
 
 }  // namespace dev
@@ -461,7 +556,18 @@ hipError_t go(const void* f, uint64_t groups, uint32_t threads, void** argv, hip
   return hipLaunchKernel(f, dim3(static_cast<uint32_t>(groups)), dim3(threads), argv, 0, stream);
 }
 
+constexpr uint32_t kMaxChunk = 64;  // a lane holds each token's pair
 constexpr uint32_t kSingleTile = 8192;  // tokens that one workgroup sorts by itself
+
+template <typename F>
+hipError_t with_rounds(uint32_t rounds, F&& f) {
+  switch (rounds) {
+    case 1: return f(Int<1>());
+    case 2: return f(Int<2>());
+    case 4: return f(Int<4>());
+    default: return f(Int<8>());
+  }
+}
 
 }  // namespace
 
@@ -484,14 +590,17 @@ EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint6
   while (vocab >> bits) ++bits;
   d.passes = (bits + 9) / 10;
   d.bits = (bits + d.passes - 1) / d.passes;
-  // sorting workgroups: one for few tokens, else up to 64
-  const uint64_t each = total <= kSingleTile ? total : (total + 63) / 64;
-  d.tile = static_cast<uint32_t>((each + 1023) / 1024 * 1024);
-  d.tiles = d.tile == 0 ? 0 : static_cast<uint32_t>((total + d.tile - 1) / d.tile);
+  // pairs a thread sorts: one workgroup for few tokens, else 64 of them while
+  // eight pairs a thread are enough
+  d.rounds = 1;
+  while (d.rounds < 8 && total > uint64_t(1024) * d.rounds * (total <= kSingleTile ? 1 : 64)) d.rounds *= 2;
+  d.tiles = static_cast<uint32_t>((total + 1024 * d.rounds - 1) / (1024 * d.rounds));
+  // with few tokens for the table's rows, all rows are cleared beside the sort
+  d.clear_all = total <= vocab / 4;
   // tokens a wave adds up: enough waves to fill the chip, few sums to join
   const uint64_t pieces = (width + vector_elems(dtype, width) * 64 - 1) / (vector_elems(dtype, width) * 64);
   d.chunk = 16;
-  while (d.chunk < 256 && total * pieces / d.chunk > 16384) d.chunk *= 2;
+  while (d.chunk < kMaxChunk && total * pieces / d.chunk > 8192) d.chunk *= 2;
   d.chunks = static_cast<uint32_t>((total + d.chunk - 1) / d.chunk);
   uint64_t at = 0;
   const auto take = [&](uint64_t bytes) {
@@ -503,8 +612,8 @@ EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint6
   d.key_b = take(total * 4);
   d.place_a = take(total * 4);
   d.place_b = take(total * 4);
-  d.hist = take(uint64_t(d.passes) * d.tiles * kMaxBins * 4);
-  d.touched = take((vocab + 31) / 32 * 4);
+  d.hist = take(uint64_t(d.tiles) * kMaxBins * 4);
+  d.touched = take((vocab + 3) / 4 * 4);
   d.partial = take(uint64_t(d.chunks) * 2 * width * 4);
   d.bytes = at;
   return d;
@@ -521,7 +630,6 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
   s.id_bytes = a.id_bytes;
   s.vocab = a.vocab;
   s.total = static_cast<uint32_t>(d.total);
-  s.tile = d.tile;
   s.tiles = d.tiles;
   s.bits = d.bits;
   s.passes = d.passes;
@@ -530,20 +638,47 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
   s.key[1] = reinterpret_cast<uint32_t*>(workspace + d.key_b);
   s.place[0] = reinterpret_cast<uint32_t*>(workspace + d.place_a);
   s.place[1] = reinterpret_cast<uint32_t*>(workspace + d.place_b);
-  s.touched = accumulate ? nullptr : reinterpret_cast<uint32_t*>(workspace + d.touched);
+  s.touched = accumulate || d.clear_all ? nullptr : workspace + d.touched;
+  uint64_t units = 0;  // pieces to clear, in equal shares by the sort's launches
+  if (!accumulate && d.clear_all) {
+    const uint64_t row = uint64_t(a.width) * (grad_dtype == kF32 ? 4 : 2);
+    for (int r = 0; r < a.P; ++r) {
+      s.clear[r] = a.out[r];
+      s.clear_bytes[r] = segment_count(a.vocab, a.P, r) * row;
+    }
+    s.clear_units = static_cast<uint32_t>((s.clear_bytes[0] + kClearUnit - 1) / kClearUnit);
+    units = uint64_t(s.clear_units) * a.P;
+  }
+  const uint32_t launches = d.tiles <= 1 ? 1 : 2 * d.passes;
+  uint32_t launch = 0;
+  // the grid of the next launch: the tiles and its share of the clearing
+  const auto grid = [&]() {
+    s.clear_first = static_cast<uint32_t>(units * launch / launches);
+    const uint32_t end = static_cast<uint32_t>(units * ++launch / launches);
+    return std::max(d.tiles, 1u) + end - s.clear_first;
+  };
   hipError_t e = hipSuccess;
   if (d.tiles <= 1) {
-    // with no tokens at all it only clears the touched bits
+    // with no tokens at all it only clears
     if (d.total == 0 && accumulate) return hipSuccess;
-    void* argv[] = {&s};
-    e = go(reinterpret_cast<const void*>(&embed_sort_all_kernel), 1, 1024, argv, stream);
+    e = with_rounds(d.rounds, [&](auto r) {
+      const uint64_t groups = grid();
+      void* argv[] = {&s};
+      return go(reinterpret_cast<const void*>(&embed_sort_all_kernel<r>), groups, 1024, argv, stream);
+    });
   } else {
-    void* argv[] = {&s};
-    e = go(reinterpret_cast<const void*>(&embed_count_kernel), d.tiles, 1024, argv, stream);
-    for (uint32_t pass = 0; e == hipSuccess && pass < d.passes; ++pass) {
-      void* pargv[] = {&s, &pass};
-      e = go(reinterpret_cast<const void*>(&embed_sort_kernel), d.tiles, 1024, pargv, stream);
-    }
+    e = with_rounds(d.rounds, [&](auto r) {
+      hipError_t f = hipSuccess;
+      for (uint32_t pass = 0; f == hipSuccess && pass < d.passes; ++pass) {
+        void* argv[] = {&s, &pass};
+        uint64_t groups = grid();
+        f = go(reinterpret_cast<const void*>(&embed_count_kernel<r>), groups, 1024, argv, stream);
+        if (f != hipSuccess) break;
+        groups = grid();
+        f = go(reinterpret_cast<const void*>(&embed_sort_kernel<r>), groups, 1024, argv, stream);
+      }
+      return f;
+    });
   }
   if (e != hipSuccess) return e;
   SumArgs m = {};
@@ -558,15 +693,17 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
   m.chunk = d.chunk;
   m.chunks = d.chunks;
   m.scale = a.scale;
-  m.key = s.key[(d.passes - 1) & 1];
-  m.place = s.place[(d.passes - 1) & 1];
+  const int sorted = d.tiles <= 1 ? 0 : (d.passes - 1) & 1;
+  m.key = s.key[sorted];
+  m.place = s.place[sorted];
   m.touched = s.touched;
+  m.accumulate = accumulate;
   m.partial = reinterpret_cast<float*>(workspace + d.partial);
   return with_type(dtype, a.width, [&](auto dt, auto ve) {
     const uint64_t pieces = (a.width + ve * 64 - 1) / (ve * 64);
     const uint64_t units = uint64_t(d.chunks) * pieces;
     m.clear_rows = std::max<uint32_t>(8, a.vocab >> 22);  // at most 2^20 workgroups
-    const uint64_t clear = accumulate ? 0 : (uint64_t(a.vocab) + 4 * m.clear_rows - 1) / (4 * m.clear_rows);
+    const uint64_t clear = accumulate || d.clear_all ? 0 : (uint64_t(a.vocab) + 4 * m.clear_rows - 1) / (4 * m.clear_rows);
     m.sum_groups = static_cast<uint32_t>((units + 3) / 4);
     const bool wide = grad_dtype == kF32 && dt != kF32;
     void* argv[] = {&m};
@@ -575,7 +712,7 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
     const void* join = wide ? reinterpret_cast<const void*>(&embed_join_kernel<dt, kF32, ve>)
                             : reinterpret_cast<const void*>(&embed_join_kernel<dt, dt, ve>);
     hipError_t r = m.sum_groups + clear == 0 ? hipSuccess : go(sum, m.sum_groups + clear, 256, argv, stream);
-    if (r == hipSuccess && d.chunks > 1) r = go(join, m.sum_groups, 256, argv, stream);
+    if (r == hipSuccess && d.chunks > 1) r = go(join, (d.chunks - 1) * pieces, 256, argv, stream);
     return r;
   });
 }

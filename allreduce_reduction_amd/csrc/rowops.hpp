@@ -91,9 +91,10 @@ struct EmbedArgs {
 // Workspace of the gradient, from the tokens' total.
 struct EmbedGradSplit {
   uint64_t total = 0;        // tokens of all ranks
-  uint32_t tile = 0, tiles = 0;  // tokens a sorting workgroup takes, sorting workgroups
+  uint32_t rounds = 0, tiles = 0;  // pairs a thread sorts, sorting workgroups
   uint32_t bits = 0, passes = 0;
   uint32_t chunk = 0, chunks = 0;  // sorted tokens a wave adds up
+  bool clear_all = false;          // clear every row, not only those without a token
   uint64_t key_a = 0, key_b = 0, place_a = 0, place_b = 0, hist = 0, touched = 0, partial = 0;  // byte offsets
   uint64_t bytes = 0;
 };
