@@ -46,27 +46,48 @@ __device__ __forceinline__ uint32_t teacher_entry(const DistillArgs& a, uint64_t
   return id >= 0 && id < static_cast<int64_t>(a.vocab) && f[0] != -__builtin_inff() ? static_cast<uint32_t>(id) : a.vocab;
 }
 
-// Maximum and sum of exponentials of a row's teacher entries; false where none counts.
-__device__ __forceinline__ bool teacher_stats(const DistillArgs& a, uint64_t row, uint32_t lane, float* top, float* sum) {
-  float m = -__builtin_inff(), s = 0.0f;
-  bool any = false;
-  for (uint32_t k = lane; k < a.top; k += 64) {
-    float t;
-    if (teacher_entry(a, row * a.top + k, &t) < a.vocab) {
-      any = true;
-      m = fmaxf(m, t);
+// A row's teacher entries: a lane's first kHeld stay in registers, so that they
+// are read once; further ones are read where they are used.
+constexpr uint32_t kHeld = 2;
+struct Teacher {
+  float t[kHeld];
+  uint32_t col[kHeld];  // vocab: does not count
+  float top, sum;       // maximum and sum of exponentials
+  __device__ __forceinline__ void load(const DistillArgs& a, uint64_t row, uint32_t lane) {
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h) {
+      col[h] = a.vocab;
+      t[h] = 0.0f;
+      if (h * 64 + lane < a.top) col[h] = teacher_entry(a, row * a.top + h * 64 + lane, &t[h]);
     }
   }
-  if (__ballot(any) == 0) return false;
-  m = wave_max(m);
-  for (uint32_t k = lane; k < a.top; k += 64) {
-    float t;
-    if (teacher_entry(a, row * a.top + k, &t) < a.vocab) s += expf(t - m);
+  // f(entry's logit / temperature, column) for the lane's entries that count.
+  template <typename F>
+  __device__ __forceinline__ void each(const DistillArgs& a, uint64_t row, uint32_t lane, F&& f) const {
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h)
+      if (col[h] < a.vocab) f(t[h], col[h]);
+    for (uint32_t k = kHeld * 64 + lane; k < a.top; k += 64) {
+      float x;
+      const uint32_t c = teacher_entry(a, row * a.top + k, &x);
+      if (c < a.vocab) f(x, c);
+    }
   }
-  *top = m;
-  *sum = wave_sum(s);
-  return true;
-}
+  // Fills top and sum; false where no entry counts.
+  __device__ __forceinline__ bool stats(const DistillArgs& a, uint64_t row, uint32_t lane) {
+    float m = -__builtin_inff(), s = 0.0f;
+    bool any = false;
+    each(a, row, lane, [&](float x, uint32_t) {
+      any = true;
+      m = fmaxf(m, x);
+    });
+    if (__ballot(any) == 0) return false;
+    top = wave_max(m);
+    each(a, row, lane, [&](float x, uint32_t) { s += expf(x - top); });
+    sum = wave_sum(s);
+    return true;
+  }
+};
 
 template <int DT>
 __device__ __forceinline__ float logit_at(const DistillArgs& a, uint64_t row, uint32_t col) {
@@ -97,7 +118,7 @@ __device__ __forceinline__ Place place_of(const DistillArgs& a, uint64_t unit, u
 // A lane's columns of a piece: kVectors vectors, and for a piece that ends its
 // rank's columns the columns past the last whole vector, one a lane.  Columns
 // that are not there read as -infinity.
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, bool STREAM>
 struct Columns {
   static constexpr int VE = Piece<DT>::VE;
   typedef Pack<DT, VE> K;
@@ -119,7 +140,7 @@ struct Columns {
 #pragma unroll
     for (uint32_t k = 0; k < kVectors; ++k) {
       if constexpr (!WHOLE) v[k] = typename K::raw{none, none, none, none};
-      if (on(k)) v[k] = K::stream(row + byte(k));
+      if (on(k)) v[k] = STREAM ? K::stream(row + byte(k)) : K::load(row + byte(k));
     }
     one = none;
     if (has_rest) one = K1::load(row + uint64_t(rest) * K::E);
@@ -131,11 +152,11 @@ struct Columns {
   }
 };
 
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, bool STREAM>
 __device__ __forceinline__ float2 piece_stats(const Place& p, const unsigned char* row, uint32_t lane, float inv) {
   constexpr int VE = Piece<DT>::VE;
   typedef Pack<DT, VE> K;
-  Columns<DT, WHOLE> c(p, lane);
+  Columns<DT, WHOLE, STREAM> c(p, lane);
   c.load(row);
   float m = WHOLE ? -__builtin_inff() : c.single();
 #pragma unroll
@@ -158,7 +179,7 @@ __device__ __forceinline__ float2 piece_stats(const Place& p, const unsigned cha
   return float2{m, wave_sum(s)};
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void distill_part_kernel(DistillArgs a) {
   const uint32_t lane = threadIdx.x & 63;
   const uint64_t units = a.rows * a.parts;
@@ -167,8 +188,8 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillArgs a) {
     const Place p = place_of(a, unit, Piece<DT>::kElems);
     const unsigned char* row = a.logits[p.rank] + p.row * p.cols * Width<DT>::bytes;
     float2 r = {-__builtin_inff(), 0.0f};
-    if (p.first + Piece<DT>::kElems <= p.cols) r = piece_stats<DT, true>(p, row, lane, inv);
-    else if (p.first < p.cols) r = piece_stats<DT, false>(p, row, lane, inv);
+    if (p.first + Piece<DT>::kElems <= p.cols) r = piece_stats<DT, true, STREAM>(p, row, lane, inv);
+    else if (p.first < p.cols) r = piece_stats<DT, false, STREAM>(p, row, lane, inv);
     if (lane == 0) a.partial[unit] = r;
   }
 }
@@ -180,6 +201,11 @@ __global__ __launch_bounds__(256) void distill_join_kernel(DistillArgs a) {
   for (uint64_t row = uint64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); row < a.rows; row += uint64_t(gridDim.x) * 4) {
     const float2* part = a.partial + row * a.parts;
     const float inv = 1.0f / a.temperature;
+    Teacher e;
+    e.load(a, row, lane);
+    float z[kHeld];  // the student's logits at the held entries
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h) z[h] = e.col[h] < a.vocab ? logit_at<DT>(a, row, e.col[h]) : 0.0f;
     float m = -__builtin_inff(), s = 0.0f;
     for (uint32_t i = lane; i < a.parts; i += 64) m = fmaxf(m, part[i].x);
     m = wave_max(m);
@@ -188,18 +214,22 @@ __global__ __launch_bounds__(256) void distill_join_kernel(DistillArgs a) {
     for (uint32_t i = lane; i < a.parts; i += 64) s += part[i].y * expf((part[i].x == -__builtin_inff() ? 0.0f : part[i].x - base) * inv);
     s = wave_sum(s);
     const float lse = base * inv + logf(s);
-    float top, sum, loss = 0.0f;
-    if (teacher_stats(a, row, lane, &top, &sum)) {
-      const float log_sum = logf(sum);
-      for (uint32_t k = lane; k < a.top; k += 64) {
+    float loss = 0.0f;
+    if (e.stats(a, row, lane)) {
+      const float log_sum = logf(e.sum);
+      const auto add = [&](float t, float logit) {
+        const float q = expf(t - e.top) / e.sum;
+        const float log_p = lse == -__builtin_inff() ? lse : logit / a.temperature - lse;
+        const float term = q * ((t - e.top) - log_sum - log_p);
+        loss += q == 0.0f ? 0.0f : term;
+      };
+#pragma unroll
+      for (uint32_t h = 0; h < kHeld; ++h)
+        if (e.col[h] < a.vocab) add(e.t[h], z[h]);
+      for (uint32_t k = kHeld * 64 + lane; k < a.top; k += 64) {
         float t;
         const uint32_t col = teacher_entry(a, row * a.top + k, &t);
-        if (col < a.vocab) {
-          const float q = expf(t - top) / sum;
-          const float log_p = lse == -__builtin_inff() ? lse : logit_at<DT>(a, row, col) / a.temperature - lse;
-          const float term = q * ((t - top) - log_sum - log_p);
-          loss += q == 0.0f ? 0.0f : term;
-        }
+        if (col < a.vocab) add(t, logit_at<DT>(a, row, col));
       }
       loss = wave_sum(loss) * a.temperature * a.temperature;
     }
@@ -223,7 +253,7 @@ __device__ __forceinline__ void wave_order() {
   __builtin_amdgcn_wave_barrier();
 }
 
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, bool STREAM>
 __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p, uint32_t lane, Entry* list) {
   constexpr int VE = Piece<DT>::VE;
   typedef Pack<DT, VE> K;
@@ -233,12 +263,13 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
   unsigned char* out = a.grads[p.rank] + off;
   const float given = a.loss_grad[p.row], by = given * a.temperature, lse = a.lse[p.row];
   const float inv = 1.0f / a.temperature;
-  Columns<DT, WHOLE> c(p, lane);
-  float top = 0.0f, sum = 1.0f;
+  Columns<DT, WHOLE, STREAM> c(p, lane);
+  Teacher teach;
   bool some = given != 0.0f;
   if (some) {
+    teach.load(a, p.row, lane);
     c.load(row);
-    some = teacher_stats(a, p.row, lane, &top, &sum);
+    some = teach.stats(a, p.row, lane);
   }
   if (!some) {
 #pragma unroll
@@ -255,16 +286,20 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
   };
   const uint32_t lo = p.rank * a.seg;
   uint32_t n = 0;
-  for (uint32_t k0 = 0; k0 < a.top; k0 += 64) {
-    float t = 0.0f;
-    const uint32_t k = k0 + lane;
-    const uint32_t col = k < a.top ? teacher_entry(a, p.row * a.top + k, &t) : a.vocab;
+  for (uint32_t h = 0; h * 64 < a.top; ++h) {
+    float t = teach.t[0];
+    uint32_t col = teach.col[0];
+    if (h == 1) t = teach.t[1], col = teach.col[1];
+    if (h >= kHeld) {
+      col = a.vocab;
+      if (h * 64 + lane < a.top) col = teacher_entry(a, p.row * a.top + h * 64 + lane, &t);
+    }
     const bool in = col < a.vocab && col >= lo + p.first && col - lo - p.first < Piece<DT>::kElems && col - lo < p.cols;
     const uint64_t who = __ballot(in);
     if (in) {
       Entry& e = list[n + __popcll(who & ((uint64_t(1) << lane) - 1))];
       e.col = col - lo;
-      e.q = expf(t - top) / sum;
+      e.q = expf(t - teach.top) / teach.sum;
     }
     n += __popcll(who);
   }
@@ -286,7 +321,10 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
     K::widen(c.v[k], f);
 #pragma unroll
     for (int i = 0; i < VE; ++i) f[i] = by * prob(f[i]);
-    if (c.on(k)) K::store(out + c.byte(k), K::narrow(f));
+    if (c.on(k)) {
+      if constexpr (STREAM) K::store_nt(out + c.byte(k), K::narrow(f));
+      else K::store(out + c.byte(k), K::narrow(f));
+    }
   }
   if (c.has_rest) {
     const float f[1] = {by * prob(c.single())};
@@ -297,15 +335,15 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
   wave_order();  // the list is free again
 }
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(256) void distill_grad_kernel(DistillArgs a) {
   extern __shared__ Entry lists[];  // [4][top]
   const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint64_t units = a.rows * a.parts;
   for (uint64_t unit = uint64_t(blockIdx.x) * 4 + wave; unit < units; unit += uint64_t(gridDim.x) * 4) {
     const Place p = place_of(a, unit, Piece<DT>::kElems);
-    if (p.first + Piece<DT>::kElems <= p.cols) piece_grad<DT, true>(a, p, lane, lists + wave * a.top);
-    else if (p.first < p.cols) piece_grad<DT, false>(a, p, lane, lists + wave * a.top);
+    if (p.first + Piece<DT>::kElems <= p.cols) piece_grad<DT, true, STREAM>(a, p, lane, lists + wave * a.top);
+    else if (p.first < p.cols) piece_grad<DT, false, STREAM>(a, p, lane, lists + wave * a.top);
   }
 }
 
@@ -319,10 +357,20 @@ hipError_t go(const void* f, uint64_t groups, uint32_t shared, void** argv, hipS
   return hipLaunchKernel(f, dim3(static_cast<uint32_t>(std::min<uint64_t>(groups, 1 << 22))), dim3(256), argv, shared, stream);
 }
 
-#define HBMC_BY_TYPE(kernel)                                                  \
-  (dtype == kF32   ? reinterpret_cast<const void*>(&kernel<kF32>)             \
-   : dtype == kF16 ? reinterpret_cast<const void*>(&kernel<kF16>)             \
-                   : reinterpret_cast<const void*>(&kernel<kBF16>))
+#define HBMC_BY_TYPE(kernel, ...)                                                        \
+  (dtype == kF32   ? reinterpret_cast<const void*>(&kernel<kF32 __VA_ARGS__>)            \
+   : dtype == kF16 ? reinterpret_cast<const void*>(&kernel<kF16 __VA_ARGS__>)            \
+                   : reinterpret_cast<const void*>(&kernel<kBF16 __VA_ARGS__>))
+#define HBMC_COMMA ,
+
+// Logits of kStreamBytes and more are read, and their gradients stored, past
+// the memory-side cache; of smaller ones the loss leaves them there for the
+// gradient.  8 ranks, bf16, 131072 columns, with and without, loss and
+// gradient: 2048 rows 87 and 100 us, 186 and 198; 256 rows 19.2 and 18.7, 30.7
+// and 25 (nontemporal stores alone 25).
+bool streams(int dtype, const DistillArgs& a) {
+  return a.rows * a.vocab * (dtype == kF32 ? 4 : 2) >= kStreamBytes;
+}
 
 }  // namespace
 
@@ -333,16 +381,21 @@ uint32_t distill_pieces(int dtype, uint64_t seg) {
 
 hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream) {
   void* argv[] = {const_cast<DistillArgs*>(&a)};
-  const hipError_t e = go(HBMC_BY_TYPE(distill_part_kernel), (a.rows * a.parts + 3) / 4, 0, argv, stream);
+  const void* part = streams(dtype, a) ? HBMC_BY_TYPE(distill_part_kernel, HBMC_COMMA true)
+                                       : HBMC_BY_TYPE(distill_part_kernel, HBMC_COMMA false);
+  const hipError_t e = go(part, (a.rows * a.parts + 3) / 4, 0, argv, stream);
   if (e != hipSuccess) return e;
   return go(HBMC_BY_TYPE(distill_join_kernel), (a.rows + 3) / 4, 0, argv, stream);
 }
 
 hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t stream) {
   void* argv[] = {const_cast<DistillArgs*>(&a)};
-  return go(HBMC_BY_TYPE(distill_grad_kernel), (a.rows * a.parts + 3) / 4, 4 * a.top * sizeof(Entry), argv, stream);
+  const void* grad = streams(dtype, a) ? HBMC_BY_TYPE(distill_grad_kernel, HBMC_COMMA true)
+                                       : HBMC_BY_TYPE(distill_grad_kernel, HBMC_COMMA false);
+  return go(grad, (a.rows * a.parts + 3) / 4, 4 * a.top * sizeof(Entry), argv, stream);
 }
 
+#undef HBMC_COMMA
 #undef HBMC_BY_TYPE
 
 }  // namespace hbmc

@@ -647,13 +647,12 @@ constexpr uint32_t kMaxGrid = 1 << 20;  // workgroups of a launch; the kernel st
 
 uint32_t up(uint32_t n, uint32_t by) { return n / by + (n % by != 0); }
 
-// Whether the ranks' copies are stored with the nontemporal hint: from 96 MiB
-// of them.  8 ranks, bf16, width 4096, with and without: 4096 rows (256 MiB)
-// 111 and 125 us, their gradient 139 and 150; 2048 rows 58 and 62, 79 and 86;
-// 1024 rows (64 MiB) 31 and 27, 47 and 47: there the cache takes the stores and
-// still holds them for whoever reads them next.
+// Whether the ranks' copies are stored with the nontemporal hint.  8 ranks,
+// bf16, width 4096, with and without: 4096 rows (256 MiB) 111 and 125 us, their
+// gradient 139 and 150; 2048 rows 58 and 62, 79 and 86; 1024 rows (64 MiB) 31
+// and 27, 47 and 47.
 bool stream_out(int dtype, const NormShape& s) {
-  return uint64_t(s.rows) * s.width * (dtype == kF32 ? 4 : 2) * s.P >= uint64_t(96) << 20;
+  return uint64_t(s.rows) * s.width * (dtype == kF32 ? 4 : 2) * s.P >= kStreamBytes;
 }
 
 }  // namespace

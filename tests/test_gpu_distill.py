@@ -81,6 +81,11 @@ def test_teacher_types(tdtype, id_dtype, tau):
     check(z, t, ids.to(id_dtype), dl, 3, tau, shift=1)
 
 
+def test_past_the_cache():
+    """Logits of 96 MiB and more are read and their gradients stored past the caches."""
+    check(*case(260, 200001, 130, "bf16"), 3, 2.0)
+
+
 def test_no_rows():
     run(*case(0, 100, 4, "bf16"), 3)
 

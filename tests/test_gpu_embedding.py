@@ -3,7 +3,7 @@ gradient) on the GPU against the formulas in 64 bits.
 
 Bounds: the lookup is one product, rounded to 32 bits and then to its type.
 The gradient of an id with m tokens adds them one after another in chunks of
-16 to 256 and then the chunks: below m + 2 additions, one product with scale
+16 to 64 and then the chunks: below m + 2 additions, one product with scale
 and one addition where it accumulates: m + 4 roundings.
 """
 import pytest
@@ -63,6 +63,11 @@ def test_lookup(P, counts, vocab, H, dtype):
 @pytest.mark.parametrize("shift", [0, 1])
 def test_lookup_ids_and_alignment(id_dtype, shift):
     lookup(3, [50, 60, 70], 999, 264, "bf16", id_dtype, -0.3, shift, "even")
+
+
+def test_lookup_past_the_cache():
+    """96 MiB of rows and more are stored past the caches."""
+    lookup(3, [9000, 1, 8000], 5000, 2997, "bf16", shift=1)
 
 
 def test_lookup_nothing():
