@@ -532,7 +532,8 @@ hbmc_status_t hbmc_graph_destroy(hbmc_graph_t graph);
  *   n = s / sqrt(mean(s^2) + post_eps) * post_weight    (s without post_weight)
  *   h = residual[t] + scale * gate[t / gate_rows] * n   (no gate: 1)
  *   out[p][t] = h / sqrt(mean(h^2) + pre_eps) * pre_weight, on every rank p
- * with every intermediate in 32 bits.  gate has ceil(rows / gate_rows) rows.
+ * with every intermediate in 32 bits (a row whose squares add up past 3.4e38
+ * has no norm).  gate has ceil(rows / gate_rows) rows.
  */
 typedef struct {
   size_t rows, width;
@@ -614,14 +615,14 @@ typedef struct {
   hbmc_dtype_t dtype;         /* of the logits and their gradients             */
   hbmc_dtype_t teacher_dtype; /* fp32, fp16 or bf16                            */
   int id_bytes;               /* 4 or 8 (signed)                               */
-  float temperature;          /* > 0                                           */
+  float temperature;          /* > 0, its square and inverse finite in 32 bits */
   const void* teacher_logits; /* [rows][top]                                   */
   const void* teacher_ids;    /* [rows][top]                                   */
 } hbmc_distill_t;
 
 /* Writes loss [rows] and lse [rows], log sum_j exp(logits_j / temperature).
  * A row whose logits are all -infinity has lse -infinity and, where an entry
- * counts, loss +infinity. */
+ * counts, loss +infinity; a NaN or +infinity among its logits gives NaN. */
 hbmc_status_t hbmc_distill_loss_workspace(hbmc_comm_t comm, const hbmc_distill_t* distill, size_t* bytes);
 hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
                                 float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -123,7 +123,7 @@ def test_gradient(P, counts, vocab, H, dtype, gdtype, accumulate):
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("kind", ["skew", "one", "none", "runs", "even"])
 @pytest.mark.parametrize("N,vocab,H", [(15, 900, 24), (1024, 1024, 24), (1025, 50001, 24), (8192, 1, 16), (8193, 70000, 16),
-                                       (40000, 2_000_000, 8), (70001, 1000, 16), (33000, 1048576, 9)])
+                                       (40000, 2_000_000, 8), (70001, 1000, 16), (33000, 1048576, 9), (540_001, 5000, 8)])
 def test_sorting(N, vocab, H, kind, accumulate):
     """One to three digits, one to 64 sorting workgroups, ids that fill whole
     chunks, cross them, and do not occur at all."""

@@ -223,3 +223,121 @@ def test_rows_past_32_bit_offsets():
         c.distill_loss([x[-50:]], t[-50:], ids[-50:], l2, e2)
         c.distill_loss_grad([x[-50:]], t[-50:], ids[-50:], e2, torch.ones(50, device="cuda"), [few])
         assert torch.equal(loss[-50:], l2) and torch.equal(lse[-50:], e2) and torch.equal(res[-50:], few)
+
+
+def guarded(t, pad=40):
+    """A copy of t on the GPU, one element past alignment, between guard zones;
+    the copy and the check that the zones are as they were."""
+    flat = torch.full((t.numel() + 2 * pad + 1,), 7, dtype=t.dtype, device="cuda")
+    view = flat[pad + 1:pad + 1 + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view, lambda: bool((flat[:pad + 1] == 7).all()) and bool((flat[pad + 1 + t.numel():] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("width", [5, 77, 1003, 2055, 9001])
+def test_nothing_outside_is_written(dtype, width):
+    g = torch.Generator().manual_seed(width)
+    ranks, rows, vocab = 3, 7, 50
+    checks = []
+
+    def buf(*shape, dt=dtype):
+        v, ok = guarded(torch.randn(*shape, generator=g).to(dt))
+        checks.append(ok)
+        return v
+
+    segs = [hi - lo for lo, hi in ref.segments(rows, ranks)]
+    cols = [hi - lo for lo, hi in ref.segments(width, ranks)]
+    vocs = [hi - lo for lo, hi in ref.segments(vocab, ranks)]
+    f32 = dict(dt=torch.float32)
+    full = lambda: [buf(rows, width) for _ in range(ranks)]  # noqa: E731
+    part = lambda: [buf(n, width) for n in segs]  # noqa: E731
+    with hc.Comm(ranks, "ring") as c:
+        w, w1 = buf(width), buf(width)
+        for gate, gate_grad in ((buf(1, width), buf(1, width, **f32)), (buf(7, width), buf(7, width, **f32))):
+            c.reduce_norm(full(), part(), full(), w, residual_out=part(), sums=part(), post_weight=w1, gate=gate)
+            c.reduce_norm_grad(full(), part(), full(), part(), w, buf(width, **f32), sums=part(), residual_grad_in=part(),
+                               post_weight=w1, post_weight_grad=buf(width, **f32), gate=gate, gate_grad=gate_grad)
+        tokens = [4, 0, 9]
+        ids = [torch.randint(-1, vocab + 1, (n,), generator=g).cuda() for n in tokens]
+        c.embedding([buf(n, width) for n in vocs], ids, [buf(n, width) for n in tokens])
+        for acc in (False, True):
+            for dt in (dtype, torch.float32):
+                c.embedding_grad([buf(n, width) for n in tokens], ids, [buf(n, width, dt=dt) for n in vocs], accumulate=acc)
+        teacher, t_ids = buf(rows, 9), torch.randint(-1, width, (rows, 9), generator=g).cuda()
+        logits, loss, lse = [buf(rows, n) for n in cols], buf(rows, **f32), buf(rows, **f32)
+        c.distill_loss(logits, teacher, t_ids, loss, lse)
+        c.distill_loss_grad(logits, teacher, t_ids, lse, buf(rows, **f32), [buf(rows, n) for n in cols])
+    torch.cuda.synchronize()
+    assert all(ok() for ok in checks)
+
+
+@pytest.mark.parametrize("rows,gate_rows,width", [(10, 4, 48), (1999, 3, 48), (700, 300, 1000), (5, 1000, 64), (531, 2, 16384)])
+def test_uneven_gate_groups(rows, gate_rows, width):
+    """The C ABI takes a last group of fewer rows."""
+    import ctypes
+    g = torch.Generator().manual_seed(rows)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF)  # noqa: E731
+    groups = -(-rows // gate_rows)
+    ranks, L = 2, hc.load_library()
+    grads, hid, sums = rnd(ranks, rows, width), rnd(rows, width), rnd(rows, width)
+    pre, post, gate = rnd(width), rnd(width), rnd(groups, width)
+    d = [t.cuda() for t in (grads, hid, sums, pre, post, gate)]
+    new = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    parts, res, y = new(ranks, rows, width, dt=BF), new(rows, width, dt=BF), new(ranks, rows, width, dt=BF)
+    dpre, dpost, dgate = new(width), new(width), new(groups, width)
+    n = hc.Norm(rows, width, gate_rows, 2, 0.5, 1e-6, 1e-6, d[3].data_ptr(), d[4].data_ptr(), d[5].data_ptr())
+    whole = lambda t: (ctypes.c_void_p * ranks)(*[t[r].data_ptr() for r in range(ranks)])  # noqa: E731
+    each = -(-rows // ranks)
+    seg = lambda t: (ctypes.c_void_p * ranks)(*[t.data_ptr() + r * each * width * 2 for r in range(ranks)])  # noqa: E731
+    need = ctypes.c_size_t()
+    with hc.Comm(ranks, "ring") as c:
+        torch.cuda.synchronize()
+        stream = torch.cuda.current_stream().cuda_stream
+        assert L.hbmc_reduce_norm(c._h, n, whole(d[0]), seg(d[1]), seg(res), whole(y), None, stream) == 0
+        f = ref.norm_forward(grads, hid, pre, post, gate, gate_rows, 0.5)
+        ref.check(y[1], f["out"], ranks + 80, "out")
+        ref.check(res, f["residual"], ranks + 80, "residual")
+        assert L.hbmc_reduce_norm_grad_workspace(c._h, n, ctypes.byref(need)) == 0
+        ws = new(need.value, dt=torch.uint8)
+        assert L.hbmc_reduce_norm_grad(c._h, n, whole(d[0]), seg(d[1]), seg(d[2]), None, whole(parts), seg(res), dpre.data_ptr(),
+                                       dpost.data_ptr(), dgate.data_ptr(), ws.data_ptr(), need.value, stream) == 0
+        b = ref.norm_backward(grads, hid, pre, sums, None, post, gate, gate_rows, 0.5)
+    for got, name in ((parts[0], "parts"), (parts[1], "parts"), (res, "residual"), (dpre, "pre"), (dpost, "post"), (dgate, "gate")):
+        ref.check(got, b[name], ranks + 180, name)
+
+
+@pytest.mark.parametrize("n", [100, 9000])
+def test_the_largest_vocabulary(n):
+    """2^30 ids (four digits to sort) of one or two columns; each id's sum in
+    the order of its tokens: below 2^-8 for the roundings to bf16 of results."""
+    vocab = 2 ** 30
+    ids = torch.randint(0, vocab, (n,), device="cuda", generator=torch.Generator("cuda").manual_seed(n))
+    ids[1::2] = vocab - 1 - ids[1::2] % 1000  # many at the far end
+    ids[0], ids[n // 2] = vocab - 1, 0
+    grads = torch.randint(-4, 5, (n, 1), device="cuda").to(BF)  # exact sums
+    table = torch.zeros(vocab, 1, dtype=BF, device="cuda")
+    with hc.Comm(1, "ring") as c:
+        c.embedding_grad([grads], [ids], [table], accumulate=True)
+        want = torch.zeros(vocab, 1, dtype=torch.float32, device="cuda").index_add_(0, ids, grads.float())
+        assert bool((table.float() - want).abs().le(2.0 ** -8 * want.abs()).all())
+        table.fill_(3)
+        c.embedding_grad([grads], [ids], [table])
+        assert bool((table.float() - want).abs().le(2.0 ** -8 * want.abs()).all())
+        got = torch.empty(n, 1, dtype=BF, device="cuda")
+        c.embedding([table], [ids], [got])
+        assert torch.equal(got, table[ids])
+
+
+def test_operators_of_every_algorithm():
+    """The algorithm of the communicator plays no part."""
+    x = torch.randn(4, 6, 80, generator=torch.Generator().manual_seed(0)).to(BF).cuda()
+    outs = []
+    for algo, kw in (("ring", {}), ("rhd", {}), ("flat", {}), ("tree", {}), ("auto", {}), ("auto_rules", {}),
+                     ("pipeline", dict(servers=2, ranks_per_server=2)), ("hier", dict(servers=2, ranks_per_server=2))):
+        with hc.Comm(4, algo, **kw) as c:
+            res = [torch.zeros(hi - lo, 80, dtype=BF, device="cuda") for lo, hi in ref.segments(6, 4)]
+            out = torch.empty_like(x)
+            c.reduce_norm(x, res, out, torch.ones(80, dtype=BF, device="cuda"))
+            outs.append(out)
+    assert all(torch.equal(o, outs[0]) for o in outs)

@@ -186,7 +186,7 @@ def distill_grad_call(c, d, lse=BASE + (40 << 20), dl=BASE + (41 << 20), **kw):
     (dict(vocab=0), BAD), (dict(vocab=2 ** 30 + 1), BAD), (dict(top=0), BAD), (dict(top=1025), UNSUPPORTED),
     (dict(dtype=3), UNSUPPORTED), (dict(teacher_dtype=4), UNSUPPORTED), (dict(dtype=7), BAD), (dict(teacher_dtype=-1), BAD),
     (dict(id_bytes=1), BAD), (dict(temperature=0.0), BAD), (dict(temperature=-1.0), BAD),
-    (dict(temperature=float("nan")), BAD), (dict(temperature=float("inf")), BAD), (dict(rows=2 ** 31), BAD),
+    (dict(temperature=1e-39), BAD), (dict(temperature=1e20), BAD), (dict(temperature=float("nan")), BAD), (dict(temperature=float("inf")), BAD), (dict(rows=2 ** 31), BAD),
     (dict(teacher_logits=None), BAD), (dict(teacher_ids=None), BAD), (dict(teacher_ids=BASE + 65540), BAD),
     (dict(teacher_logits=BASE + 2), BAD),
 ])
