@@ -196,50 +196,98 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillArgs a) {
   }
 }
 
-// Joins a row's pieces and adds the teacher's terms: one wave a row.
+// A row's teacher entries and the student's logits at the held ones.
+template <int DT>
+struct RowEntries {
+  Teacher e;
+  float z[kHeld];
+  __device__ __forceinline__ void load(const DistillArgs& a, uint64_t row, uint32_t lane) {
+    e.load(a, row, lane);
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h) z[h] = e.col[h] < a.vocab ? logit_at<DT>(a, row, e.col[h]) : 0.0f;
+  }
+};
+
+// One wave: joins a row's (maximum, sum) pairs, adds the teacher's terms and
+// stores the row's loss and log-sum-exp.
+template <int DT>
+__device__ __forceinline__ void finish_row(const DistillArgs& a, uint64_t row, uint32_t lane, const float2* part, uint32_t parts,
+                                           RowEntries<DT>& entries) {
+  Teacher& e = entries.e;
+  const float (&z)[kHeld] = entries.z;
+  const float inv = 1.0f / a.temperature;
+  float m = -__builtin_inff(), s = 0.0f;
+  for (uint32_t i = lane; i < parts; i += 64) m = fmaxf(m, part[i].x);
+  m = wave_max(m);
+  const float base = m == -__builtin_inff() ? 0.0f : m;
+  // a piece of -inf alone has the sum 0 (or NaN)
+  for (uint32_t i = lane; i < parts; i += 64)
+    s += part[i].y * expf((part[i].x == -__builtin_inff() ? 0.0f : part[i].x - base) * inv);
+  s = wave_sum(s);
+  const float lse = base * inv + logf(s);
+  float loss = 0.0f;
+  if (e.stats(a, row, lane)) {
+    const float log_sum = logf(e.sum), inv_sum = 1.0f / e.sum;
+    const auto add = [&](float t, float logit) {
+      const float q = exp_fast(t - e.top) * inv_sum;
+      const float log_p = lse == -__builtin_inff() ? lse : logit * inv - lse;
+      const float term = q * ((t - e.top) - log_sum - log_p);
+      loss += q == 0.0f ? 0.0f : term;
+    };
+#pragma unroll
+    for (uint32_t h = 0; h < kHeld; ++h)
+      if (e.col[h] < a.vocab) add(e.t[h], z[h]);
+    for (uint32_t k = kHeld * 64 + lane; k < a.top; k += 64) {
+      float t;
+      const uint32_t col = teacher_entry(a, row * a.top + k, &t);
+      if (col < a.vocab) add(t, logit_at<DT>(a, row, col));
+    }
+    loss = wave_sum(loss) * a.temperature * a.temperature;
+  }
+  if (lane == 0) {
+    a.loss[row] = loss;
+    a.lse[row] = lse;
+  }
+}
+
+// Joins the pieces of distill_part_kernel: one wave a row.
 template <int DT>
 __global__ __launch_bounds__(256) void distill_join_kernel(DistillArgs a) {
   const uint32_t lane = threadIdx.x & 63;
   for (uint64_t row = uint64_t(blockIdx.x) * 4 + uniform(threadIdx.x >> 6); row < a.rows; row += uint64_t(gridDim.x) * 4) {
-    const float2* part = a.partial + row * a.parts;
-    const float inv = 1.0f / a.temperature;
-    Teacher e;
-    e.load(a, row, lane);
-    float z[kHeld];  // the student's logits at the held entries
-#pragma unroll
-    for (uint32_t h = 0; h < kHeld; ++h) z[h] = e.col[h] < a.vocab ? logit_at<DT>(a, row, e.col[h]) : 0.0f;
-    float m = -__builtin_inff(), s = 0.0f;
-    for (uint32_t i = lane; i < a.parts; i += 64) m = fmaxf(m, part[i].x);
-    m = wave_max(m);
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    // a piece of -inf alone has the sum 0 (or NaN)
-    for (uint32_t i = lane; i < a.parts; i += 64) s += part[i].y * expf((part[i].x == -__builtin_inff() ? 0.0f : part[i].x - base) * inv);
-    s = wave_sum(s);
-    const float lse = base * inv + logf(s);
-    float loss = 0.0f;
-    if (e.stats(a, row, lane)) {
-      const float log_sum = logf(e.sum), inv_sum = 1.0f / e.sum;
-      const auto add = [&](float t, float logit) {
-        const float q = exp_fast(t - e.top) * inv_sum;
-        const float log_p = lse == -__builtin_inff() ? lse : logit * inv - lse;
-        const float term = q * ((t - e.top) - log_sum - log_p);
-        loss += q == 0.0f ? 0.0f : term;
-      };
-#pragma unroll
-      for (uint32_t h = 0; h < kHeld; ++h)
-        if (e.col[h] < a.vocab) add(e.t[h], z[h]);
-      for (uint32_t k = kHeld * 64 + lane; k < a.top; k += 64) {
-        float t;
-        const uint32_t col = teacher_entry(a, row * a.top + k, &t);
-        if (col < a.vocab) add(t, logit_at<DT>(a, row, col));
-      }
-      loss = wave_sum(loss) * a.temperature * a.temperature;
-    }
-    if (lane == 0) {
-      a.loss[row] = loss;
-      a.lse[row] = lse;
-    }
+    RowEntries<DT> entries;
+    entries.load(a, row, lane);
+    finish_row<DT>(a, row, lane, a.partial + row * a.parts, a.parts, entries);
   }
+}
+
+// The whole loss of few short rows in one launch: a workgroup a row, a wave
+// every 16th piece.
+constexpr uint32_t kRowWaves = 16;
+template <int DT>
+__global__ __launch_bounds__(64 * kRowWaves) void distill_row_kernel(DistillArgs a) {
+  __shared__ float2 pairs[kRowWaves];
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint64_t row = blockIdx.x;
+  const float inv = 1.0f / a.temperature;
+  RowEntries<DT> entries;
+  if (wave == 0) entries.load(a, row, lane);
+  float2 all = {-__builtin_inff(), 0.0f};
+  for (uint32_t part = wave; part < a.parts; part += kRowWaves) {
+    const Place p = place_of(a, row * a.parts + part, Piece<DT>::kElems);
+    if (p.first >= p.cols) continue;
+    const unsigned char* at = a.logits[p.rank] + row * p.cols * Width<DT>::bytes;
+    const float2 r = p.first + Piece<DT>::kElems <= p.cols ? piece_stats<DT, true, false>(p, at, lane, inv)
+                                                           : piece_stats<DT, false, false>(p, at, lane, inv);
+    // (m, s) pairs joined relative to their larger maximum; -infinity adds nothing but a NaN
+    const float m = fmaxf(all.x, r.x), base = m == -__builtin_inff() ? 0.0f : m;
+    all.y = all.y * exp_fast(((all.x == -__builtin_inff() ? base : all.x) - base) * inv) +
+            r.y * exp_fast(((r.x == -__builtin_inff() ? base : r.x) - base) * inv);
+    all.x = m;
+  }
+  if (lane == 0) pairs[wave] = all;
+  __syncthreads();
+  if (wave == 0) finish_row<DT>(a, row, lane, pairs, kRowWaves, entries);
 }
 
 // A teacher entry of a wave's piece: its column on the rank, its q, and the
@@ -362,6 +410,8 @@ hipError_t go(const void* f, uint64_t groups, uint32_t shared, void** argv, hipS
   return hipLaunchKernel(f, dim3(static_cast<uint32_t>(std::min<uint64_t>(groups, 1 << 22))), dim3(256), argv, shared, stream);
 }
 
+constexpr uint64_t kFewRows = 512, kShortRow = uint64_t(256) << 10;
+
 #define HBMC_BY_TYPE(kernel, ...)                                                        \
   (dtype == kF32   ? reinterpret_cast<const void*>(&kernel<kF32 __VA_ARGS__>)            \
    : dtype == kF16 ? reinterpret_cast<const void*>(&kernel<kF16 __VA_ARGS__>)            \
@@ -377,7 +427,21 @@ bool streams(int dtype, const DistillArgs& a) {
   return a.rows * a.vocab * (dtype == kF32 ? 4 : 2) >= kStreamBytes;
 }
 
+// Whether a loss takes one launch, a workgroup a row, instead of a launch for
+// pieces and one that joins them.  8 ranks, 64 entries, one and two launches,
+// us: one bf16 row of 32000 columns 6 and 11.5, of 131072 (256 KiB) 10.4 and
+// 11.5; 256 rows of 32000 7.5 and 11.6, of 131072 14.8 and 18.5; 512 rows 12.7
+// and 14, 30.7 and 30.7; 1024 rows of 32000 22.5 and 19.3; one fp32 row of
+// 262144 (1 MiB) 19 and 11.8.
+bool by_rows(int dtype, const DistillArgs& a) {
+  return a.rows <= kFewRows && uint64_t(a.vocab) * (dtype == kF32 ? 4 : 2) <= kShortRow;
+}
+
 }  // namespace
+
+uint64_t distill_workspace(int dtype, const DistillArgs& a) {
+  return by_rows(dtype, a) ? 0 : a.rows * a.parts * sizeof(float2);
+}
 
 uint32_t distill_pieces(int dtype, uint64_t seg) {
   const uint32_t elems = dtype == kF32 ? Piece<kF32>::kElems : Piece<kF16>::kElems;
@@ -386,6 +450,8 @@ uint32_t distill_pieces(int dtype, uint64_t seg) {
 
 hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream) {
   void* argv[] = {const_cast<DistillArgs*>(&a)};
+  if (by_rows(dtype, a))
+    return hipLaunchKernel(HBMC_BY_TYPE(distill_row_kernel), dim3(static_cast<uint32_t>(a.rows)), dim3(64 * kRowWaves), argv, 0, stream);
   const void* part = streams(dtype, a) ? HBMC_BY_TYPE(distill_part_kernel, HBMC_COMMA true)
                                        : HBMC_BY_TYPE(distill_part_kernel, HBMC_COMMA false);
   const hipError_t e = go(part, (a.rows * a.parts + 3) / 4, 0, argv, stream);

@@ -289,8 +289,6 @@ hbmc_status_t distill_args(hbmc_comm_t comm, const hbmc_distill_t* m, DistillArg
   return HBMC_OK;
 }
 
-uint64_t distill_bytes(const DistillArgs& a) { return a.rows * a.parts * sizeof(float2); }
-
 void read_teacher(const DistillArgs& a, Ranges* r) {
   const uint32_t te = float_bytes(a.teacher_dtype);
   r->read(a.teacher, a.rows * a.top * te, te);
@@ -302,7 +300,8 @@ hbmc_status_t distill_loss(hbmc_comm_t comm, const hbmc_distill_t* m, const void
   DistillArgs a = {};
   hbmc_status_t st = distill_args(comm, m, &a);
   if (st != HBMC_OK) return st;
-  if (!logits || workspace_bytes < distill_bytes(a)) return HBMC_ERR_INVALID_ARG;
+  const uint64_t bytes = distill_workspace(m->dtype, a);
+  if (!logits || workspace_bytes < bytes) return HBMC_ERR_INVALID_ARG;
   const uint32_t e = float_bytes(m->dtype);
   Ranges r;
   read_teacher(a, &r);
@@ -312,7 +311,7 @@ hbmc_status_t distill_loss(hbmc_comm_t comm, const hbmc_distill_t* m, const void
   }
   r.write(loss, a.rows * 4, 4);
   r.write(lse, a.rows * 4, 4);
-  r.write(workspace, distill_bytes(a), 16);
+  r.write(workspace, bytes, 16);
   if (!r.ok()) return HBMC_ERR_INVALID_ARG;
   if (a.rows == 0) return HBMC_OK;
   a.loss = loss;
@@ -404,7 +403,7 @@ hbmc_status_t hbmc_distill_loss_workspace(hbmc_comm_t comm, const hbmc_distill_t
     DistillArgs a = {};
     if (!bytes) return HBMC_ERR_INVALID_ARG;
     const hbmc_status_t st = distill_args(comm, distill, &a);
-    if (st == HBMC_OK) *bytes = distill_bytes(a);
+    if (st == HBMC_OK) *bytes = distill_workspace(distill->dtype, a);
     return st;
   });
 }

@@ -131,6 +131,7 @@ struct DistillArgs {
 };
 // Pieces of a row's columns that the loss kernels take one workgroup each.
 uint32_t distill_pieces(int dtype, uint64_t seg);
+uint64_t distill_workspace(int dtype, const DistillArgs& a);  // bytes of the loss
 hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream);
 hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t stream);
 

@@ -68,6 +68,8 @@ def check(z, t, ids, dl, P, tau=1.0, shift=0):
 @pytest.mark.parametrize("P,n,vocab,k", [
     (8, 1, 32768, 64), (4, 7, 50001, 20), (1, 3, 1, 1), (3, 5, 2, 2), (5, 33, 1003, 64), (16, 2, 100, 100), (2, 2, 8192, 1024),
     (1, 4, 4096, 65), (1, 4, 4097, 1), (1, 2, 20000, 1000), (64, 3, 640, 8), (7, 129, 333, 3), (2, 3, 16, 40),
+    # pieces and their joining in two launches: many rows, or long ones
+    (5, 600, 1003, 64), (3, 513, 9001, 300), (1, 600, 4097, 7), (64, 513, 100, 2), (2, 3, 140001, 1000), (3, 1, 270000, 260),
 ])
 def test_shapes(P, n, vocab, k, dtype):
     check(*case(n, vocab, k, dtype), P, 2.0 if k > 1 else 1.0)
@@ -90,10 +92,11 @@ def test_no_rows():
     run(*case(0, 100, 4, "bf16"), 3)
 
 
-def test_masks():
+@pytest.mark.parametrize("rows", [12, 600])
+def test_masks(rows):
     """Entries that do not count, rows in which none does, padding rows whose
     logits hold anything, masked logits, the same column twice."""
-    z, t, ids, dl = case(12, 9000, 16, "bf16", seed=4)
+    z, t, ids, dl = case(rows, 9000, 16, "bf16", seed=4)
     ids[0, 3:] = -1
     ids[1] = -1
     ids[2, 5], ids[2, 6] = 9000, 2 ** 40
@@ -117,10 +120,11 @@ def test_masks():
     assert not torch.isnan(grads).any()
 
 
-def test_nothing_left():
+@pytest.mark.parametrize("rows", [3, 513])
+def test_nothing_left(rows):
     """A masked teacher column: infinite loss, and a gradient without NaN; a
     row of -infinity alone has no distribution and p counts as zero."""
-    z, t, ids, dl = case(3, 600, 8, "fp32", seed=2)
+    z, t, ids, dl = case(rows, 600, 8, "fp32", seed=2)
     z[0, ids[0, 2]] = -torch.inf
     z[1] = -torch.inf
     loss, lse, grads = run(z, t, ids, dl, 3)
@@ -129,10 +133,11 @@ def test_nothing_left():
     ref.check(grads, ref.distill_backward(z, t, ids, 1.0, dl, lse.cpu()), 40, "grads")
 
 
-def test_large_values():
+@pytest.mark.parametrize("rows", [2, 520])
+def test_large_values(rows):
     """Logits of the size of fp32's and fp16's ends do not overflow."""
     for dtype, big in (("fp16", 60000.0), ("fp32", 1e30)):
-        z, t, ids, dl = case(2, 3000, 5, dtype)
+        z, t, ids, dl = case(rows, 3000, 5, dtype)
         z[0, 100], z[0, 200] = big, -big
         ids[0, 0] = 100
         loss, lse, grads = run(z, t, ids, dl, 2)

@@ -200,14 +200,16 @@ def test_distill_buffers(comm):
     assert distill_call(comm, distill_args(rows=0, teacher_logits=None, teacher_ids=None), loss=None, lse=None, ws=None,
                         bytes_=0, logits=ptrs(4, 0, 0)) == OK
     assert distill_call(comm, None) == BAD and distill_grad_call(comm, None) == BAD
-    for kw in (dict(loss=None), dict(lse=None), dict(logits=None), dict(logits=ptrs(4, 0, 0)), dict(ws=None),
-               dict(lse=BASE + (40 << 20) + 4), dict(loss=BASE + (1 << 20)), dict(loss=BASE + (39 << 20) + 2),
-               dict(ws=BASE + (1 << 31) + 4), dict(ws=BASE + (1 << 20))):
+    for kw in (dict(loss=None), dict(lse=None), dict(logits=None), dict(logits=ptrs(4, 0, 0)),
+               dict(lse=BASE + (40 << 20) + 4), dict(loss=BASE + (1 << 20)), dict(loss=BASE + (39 << 20) + 2)):
         assert distill_call(comm, d, **kw) == BAD, kw
-    need = ctypes.c_size_t()
-    assert L.hbmc_distill_loss_workspace(comm._h, d, ctypes.byref(need)) == OK and need.value > 0
+    need = ctypes.c_size_t(1)
+    assert L.hbmc_distill_loss_workspace(comm._h, d, ctypes.byref(need)) == OK and need.value == 0  # one launch
     assert L.hbmc_distill_loss_workspace(comm._h, d, None) == BAD
-    assert distill_call(comm, d, bytes_=need.value - 1) == BAD
+    many = distill_args(rows=5000, teacher_logits=BASE + (50 << 20), teacher_ids=BASE + (60 << 20))
+    assert L.hbmc_distill_loss_workspace(comm._h, many, ctypes.byref(need)) == OK and need.value > 0
+    for kw in (dict(bytes_=need.value - 1), dict(ws=None), dict(ws=BASE + (1 << 31) + 4), dict(ws=BASE + (1 << 20))):
+        assert distill_call(comm, many, **kw) == BAD, kw
     for kw in (dict(lse=None), dict(dl=None), dict(grads=None), dict(logits=None), dict(grads=ptrs(4, 0, 0)),
                dict(grads=ptrs(4, BASE + (1 << 20) + 2, 1 << 20)), dict(grads=ptrs(4, BASE + (8 << 20), 64)),
                dict(dl=BASE + (8 << 20))):
