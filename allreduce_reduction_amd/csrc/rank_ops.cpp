@@ -263,7 +263,7 @@ hbmc_status_t embedding_grad(hbmc_comm_t comm, const hbmc_embedding_t* m, const 
 
 // ------------------------------------------------------------ distillation
 
-hbmc_status_t distill_args(hbmc_comm_t comm, const hbmc_distill_t* m, DistillArgs* a) {
+hbmc_status_t distill_args(hbmc_comm_t comm, const hbmc_distill_t* m, bool grad, DistillArgs* a) {
   const int P = ranks_of(comm);
   if (P == 0 || !m) return HBMC_ERR_INVALID_ARG;
   for (const int t : {static_cast<int>(m->dtype), static_cast<int>(m->teacher_dtype)})
@@ -284,8 +284,9 @@ hbmc_status_t distill_args(hbmc_comm_t comm, const hbmc_distill_t* m, DistillArg
   a->temperature = m->temperature;
   a->teacher = static_cast<const unsigned char*>(m->teacher_logits);
   a->ids = static_cast<const unsigned char*>(m->teacher_ids);
-  a->pieces = distill_pieces(m->dtype, a->seg);
+  a->pieces = distill_pieces(m->dtype, grad, a->seg);
   a->parts = a->pieces * static_cast<uint32_t>(P);
+  if (a->rows * a->pieces > UINT32_MAX - 4) return HBMC_ERR_UNSUPPORTED;  // far past any memory
   return HBMC_OK;
 }
 
@@ -298,7 +299,7 @@ void read_teacher(const DistillArgs& a, Ranges* r) {
 hbmc_status_t distill_loss(hbmc_comm_t comm, const hbmc_distill_t* m, const void* const logits[], float* loss, float* lse,
                            void* workspace, size_t workspace_bytes, void* stream) {
   DistillArgs a = {};
-  hbmc_status_t st = distill_args(comm, m, &a);
+  hbmc_status_t st = distill_args(comm, m, false, &a);
   if (st != HBMC_OK) return st;
   const uint64_t bytes = distill_workspace(m->dtype, a);
   if (!logits || workspace_bytes < bytes) return HBMC_ERR_INVALID_ARG;
@@ -323,7 +324,7 @@ hbmc_status_t distill_loss(hbmc_comm_t comm, const hbmc_distill_t* m, const void
 hbmc_status_t distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* m, const void* const logits[], const float* lse,
                                 const float* loss_grad, void* const logit_grads[], void* stream) {
   DistillArgs a = {};
-  hbmc_status_t st = distill_args(comm, m, &a);
+  hbmc_status_t st = distill_args(comm, m, true, &a);
   if (st != HBMC_OK) return st;
   if (!logits || !logit_grads) return HBMC_ERR_INVALID_ARG;
   const uint32_t e = float_bytes(m->dtype);
@@ -402,7 +403,7 @@ hbmc_status_t hbmc_distill_loss_workspace(hbmc_comm_t comm, const hbmc_distill_t
   return no_throw([&]() -> hbmc_status_t {
     DistillArgs a = {};
     if (!bytes) return HBMC_ERR_INVALID_ARG;
-    const hbmc_status_t st = distill_args(comm, distill, &a);
+    const hbmc_status_t st = distill_args(comm, distill, false, &a);
     if (st == HBMC_OK) *bytes = distill_workspace(distill->dtype, a);
     return st;
   });

@@ -129,8 +129,8 @@ struct DistillArgs {
   float2* partial;  // [rows][parts]: (maximum, sum) of a piece of a rank's columns
   uint32_t parts, pieces;  // pieces of a rank's columns, pieces of all ranks
 };
-// Pieces of a row's columns that the loss kernels take one workgroup each.
-uint32_t distill_pieces(int dtype, uint64_t seg);
+// Pieces of a rank's columns of a row, a wave's work each.
+uint32_t distill_pieces(int dtype, bool grad, uint64_t seg);
 uint64_t distill_workspace(int dtype, const DistillArgs& a);  // bytes of the loss
 hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream);
 hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t stream);
