@@ -3,7 +3,7 @@ gradient) on the GPU against the formulas in 64 bits.
 
 Bounds: the lookup is one product, rounded to 32 bits and then to its type.
 The gradient of an id with m tokens adds them one after another in chunks of
-16 to 64 and then the chunks: below m + 2 additions, one product with scale
+8 to 64 and then the chunks: below m + 2 additions, one product with scale
 and one addition where it accumulates: m + 4 roundings.
 """
 import pytest
