@@ -1,10 +1,19 @@
 // The norms before and after a block's end over the ranks' partial sums, with
 // gate and residual scale, and their gradient (see hbmc_reduce_norm).
 //
+//   s = sum of the ranks' rows        r1 = 1 / rms(s)     n = s * r1 * w1
+//   h = residual + scale * gate * n   r2 = 1 / rms(h)     out = h * r2 * w2
+// and back, with g the sum of the ranks' gradients and a = g * w2,
+//   dh = r2 * a - h * r2^3 * mean(a * h) + dresidual_out
+//   b = scale * gate * w1 * dh        ds = r1 * b - s * r1^3 * mean(b * s)
+//
 // Both directions stream: a row is P operand rows in, P copies out and a few
 // rows of one rank, each touched once, with every row statistic taken from
-// registers.  What bounds them is HBM (a decode step's single row: the launch
-// and one round trip).
+// registers.  What bounds them is HBM, at the rate of as many streams written as
+// read: 4096 rows of 4096 bf16 over 8 ranks move 638 MB forward in 111 us (5.7
+// TB/s) and 671 MB backward in 139 (4.8, 5.2 without the joining of the weights'
+// gradients); a copy of one stream reaches 7.  One row alone takes 5.6 us: the
+// launch and one round trip.
 #include <algorithm>
 
 #include "rowops.hpp"
@@ -12,11 +21,11 @@
 namespace hbmc {
 namespace dev {
 
-// A row is held by WAVES waves, VPT vectors of VE elements a lane.  Rows of 16 waves (kWide) have 128
-// registers a lane: they read weights, and in the gradient the row's own
-// operands, again where they are used (from L2) instead of holding them, and
-// keep two of the three weight gradients in LDS.
-// SLOTS rows share a workgroup.
+// A row is held by WAVES waves, VPT vectors of VE elements a lane; SLOTS rows
+// share a workgroup.  Rows of 16 waves (kWide) have 128 registers a lane: they
+// read weights, and in the gradient the row's own operands, again where they are
+// used (from L2) instead of holding them, and keep the gradient's sums over the
+// rows in LDS.
 template <int WAVES, int SLOTS>
 struct RowTile {
   static constexpr int kThreads = 64 * WAVES;
