@@ -204,8 +204,8 @@ __global__ __launch_bounds__(256) void distill_part_kernel(DistillArgs a) {
     const Place p = place_of(a, unit, Piece<DT, kLossVectors>::kElems);
     const unsigned char* row = a.logits[p.rank] + p.row * p.cols * Width<DT>::bytes;
     float2 r = {-__builtin_inff(), 0.0f};
-    if (p.first < p.cols && p.limit - p.first == Piece<DT, kLossVectors>::kElems) r = piece_stats<DT, true, STREAM>(p, row, lane, inv);
-    else if (p.first < p.cols) r = piece_stats<DT, false, STREAM>(p, row, lane, inv);
+    const bool whole = p.limit - p.first == Piece<DT, kLossVectors>::kElems;
+    if (p.first < p.cols) r = whole ? piece_stats<DT, true, STREAM>(p, row, lane, inv) : piece_stats<DT, false, STREAM>(p, row, lane, inv);
     if (lane == 0) a.partial[p.row * a.parts + p.rank * a.pieces + p.first / Piece<DT, kLossVectors>::kElems] = r;
   }
 }
@@ -292,8 +292,8 @@ __global__ __launch_bounds__(64 * kRowWaves) void distill_row_kernel(DistillArgs
     const Place p = place_of(a, static_cast<uint32_t>(row), rank, part - rank * a.pieces, Piece<DT, kLossVectors>::kElems);
     if (p.first >= p.cols) continue;
     const unsigned char* at = a.logits[p.rank] + row * p.cols * Width<DT>::bytes;
-    const float2 r = p.limit - p.first == Piece<DT, kLossVectors>::kElems ? piece_stats<DT, true, false>(p, at, lane, inv)
-                                                           : piece_stats<DT, false, false>(p, at, lane, inv);
+    const bool whole = p.limit - p.first == Piece<DT, kLossVectors>::kElems;
+    const float2 r = whole ? piece_stats<DT, true, false>(p, at, lane, inv) : piece_stats<DT, false, false>(p, at, lane, inv);
     // (m, s) pairs joined relative to their larger maximum; -infinity adds nothing but a NaN
     const float m = fmaxf(all.x, r.x), base = m == -__builtin_inff() ? 0.0f : m;
     all.y = all.y * exp_fast(((all.x == -__builtin_inff() ? base : all.x) - base) * inv) +
@@ -343,13 +343,14 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
     if (c.has_rest) K1::store(out + uint64_t(c.rest) * K::E, 0);
     return;
   }
-  // p, zero throughout where lse is -infinity.  16-bit gradients take 2^(z * c -
-  // lse * log2 e) in one fused product: its rounding, some 2^-19 of p for |z| /
-  // temperature and lse of 30, is far below theirs.
-  const float scale2 = inv * kLog2e, shift2 = lse == -__builtin_inff() ? lse : -lse * kLog2e;
+  // p, zero throughout where lse is -infinity.  The difference is taken before
+  // the factor log2 e: with logits at the type's lowest value either product
+  // alone would overflow.
+  const float shift = lse == -__builtin_inff() ? lse : -lse;
   const auto prob = [&](float z) {
-    if constexpr (DT == kF32) return lse == -__builtin_inff() ? 0.0f : expf(z * inv - lse);
-    else return __builtin_amdgcn_exp2f(__builtin_fmaf(z, scale2, shift2));
+    const float x = __builtin_fmaf(z, inv, shift);
+    if constexpr (DT == kF32) return expf(x);
+    else return exp_fast(x);
   };
   const uint32_t lo = p.rank * a.seg;
   const float inv_sum = 1.0f / teach.sum;
@@ -414,8 +415,10 @@ __global__ __launch_bounds__(256) void distill_grad_kernel(DistillArgs a) {
     const uint32_t unit = block * 4 + wave;
     if (unit >= units) return;
     const Place p = place_of(a, unit, Piece<DT, kGradVectors>::kElems);
-    if (p.first < p.cols && p.limit - p.first == Piece<DT, kGradVectors>::kElems) piece_grad<DT, true, STREAM>(a, p, lane, lists + wave * a.top);
-    else if (p.first < p.cols) piece_grad<DT, false, STREAM>(a, p, lane, lists + wave * a.top);
+    if (p.first >= p.cols) continue;
+    const bool whole = p.limit - p.first == Piece<DT, kGradVectors>::kElems;
+    if (whole) piece_grad<DT, true, STREAM>(a, p, lane, lists + wave * a.top);
+    else piece_grad<DT, false, STREAM>(a, p, lane, lists + wave * a.top);
   }
 }
 

@@ -570,8 +570,8 @@ hbmc_status_t hbmc_reduce_norm_grad(hbmc_comm_t comm, const hbmc_norm_t* norm, c
                                     void* const residual_grad[], float* pre_weight_grad, float* post_weight_grad,
                                     float* gate_grad, void* workspace, size_t workspace_bytes, void* stream);
 
-/* An embedding of `vocab` rows (1 .. 2^30) of `width` elements, rank r holding
- * the rows it owns. */
+/* An embedding of `vocab` rows (1 .. 2^30) of `width` elements (1 .. 2^24), rank
+ * r holding the rows it owns. */
 typedef struct {
   size_t vocab, width;
   hbmc_dtype_t dtype;
@@ -580,7 +580,7 @@ typedef struct {
 } hbmc_embedding_t;
 
 /* out[p][t] = scale * row ids[p][t] of the table, for the tokens[p] (below
- * 2^26) tokens of each rank p; ids outside [0, vocab) give rows of zeros.
+ * 2^26, below 2^31 in all) tokens of each rank p; ids outside [0, vocab) give rows of zeros.
  * tables[r]: the rows that rank r owns.  The ranks' ids may be one buffer. */
 hbmc_status_t hbmc_embedding(hbmc_comm_t comm, const hbmc_embedding_t* emb, const void* const tables[],
                              const void* const ids[], const size_t tokens[], void* const out[], void* stream);
@@ -630,8 +630,9 @@ hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill,
 /* logit_grads[r][t][j] = loss_grad[t] * temperature * (p_j - the sum of q_k
  * over the entries with column j), from the forward call's lse; zeros for a
  * row whose loss_grad is zero or that has no counting entry, whatever its
- * logits hold; p is zero in a row whose lse is -infinity.  logit_grads[r] may
- * be logits[r]. */
+ * logits hold; p is zero in a row whose lse is -infinity, and comes from lse as
+ * it is, in 32 bits (a row that holds the type's lowest value alone has p = 1
+ * throughout).  logit_grads[r] may be logits[r]. */
 hbmc_status_t hbmc_distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
                                      const float* lse, const float* loss_grad, void* const logit_grads[],
                                      void* stream);

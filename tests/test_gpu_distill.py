@@ -109,7 +109,11 @@ def test_masks(rows):
     ids[8, :8] = -(2 ** 63)
     z[9] = torch.finfo(torch.bfloat16).min  # masked by the type's lowest value
     z[9, ids[9]] = 1.0
+    z[11] = torch.finfo(torch.bfloat16).min  # in every column
     check(z, t, ids, dl, 4, 1.5)
+    check(z, t, ids, dl, 4, 1.0)
+    loss, lse, grads = run(z, t, ids, dl, 4)
+    assert torch.isfinite(loss).all() and torch.isfinite(lse).all() and torch.isfinite(grads).all()
     dl[10] = 0
     z[10] = float("nan")
     ids[1] = -1
