@@ -518,8 +518,9 @@ hbmc_status_t hbmc_graph_destroy(hbmc_graph_t graph);
  *     must not overlap any other buffer of the call unless stated;
  *   - `workspace` is scratch memory of at least the bytes the matching
  *     ..._workspace call (host only) reports, 16-byte aligned, the caller's
- *     own (NULL for none), free to reuse once the call's work on `stream` is done.  Calls that
- *     may run at the same time, replayed graphs included, need one each;
+ *     own (NULL for none), free to reuse once the call's work on `stream` is
+ *     done.  Calls that may run at the same time, replayed graphs included,
+ *     need one each;
  *   - nothing is allocated, cached or synchronised: every call may be
  *     captured into a graph, the first one included;
  *   - the same inputs give the same bits on every run.
@@ -580,7 +581,8 @@ typedef struct {
 } hbmc_embedding_t;
 
 /* out[p][t] = scale * row ids[p][t] of the table, for the tokens[p] (below
- * 2^26, below 2^31 in all) tokens of each rank p; ids outside [0, vocab) give rows of zeros.
+ * 2^26, below 2^31 in all) tokens of each rank p; ids outside [0, vocab) give
+ * rows of zeros.
  * tables[r]: the rows that rank r owns.  The ranks' ids may be one buffer. */
 hbmc_status_t hbmc_embedding(hbmc_comm_t comm, const hbmc_embedding_t* emb, const void* const tables[],
                              const void* const ids[], const size_t tokens[], void* const out[], void* stream);
