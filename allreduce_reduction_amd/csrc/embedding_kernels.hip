@@ -14,7 +14,8 @@
 // fixed.  It reads each gradient row once.  32768 tokens of 4096 bf16 added to
 // 65536 fp32 rows take 157 us: the sort 25 us (four launches of one round trip
 // or two each), the sums 118 us (their 0.6 GB at 5.4 TB/s: tokens' rows and the
-// table's lie scattered), the joining 7 to 10 us.
+// table's lie scattered), the joining 7 to 10 us.  Few tokens take one launch
+// without sorting (embed_few_kernel).
 #include <algorithm>
 
 #include "rowops.hpp"
@@ -539,6 +540,155 @@ __global__ __launch_bounds__(256) void embed_join_kernel(SumArgs a) {
   write_row<GT, VE>(a, key, c, acc, old);
 }
 
+// ------------------------------------------------------------- few tokens
+
+// A call of few tokens in one launch, with no sort and no workspace: a workgroup
+// for each token and `per` pieces of a row asks every token for its id; the first
+// token of an id adds up all of that id's, in the tokens' order, and the others
+// leave.  Most ids occur once or a few times: a wave then takes a piece; more than
+// kAlone * per tokens are dealt out to the four waves, piece by piece.  The
+// workgroups past those clear the rows that have no token.  8 ranks, bf16 into
+// fp32, added: 64 tokens of 4096 6.8 us and 512 of 2048 8.2 us, where the sort's
+// three launches take 18 and 20; what bounds it is a chain of four round trips
+// (ranks' tokens, ids, gradient rows, stores) and, from 1000 workgroups on, that
+// each reads all ids.
+struct FewArgs {
+  SortArgs t;
+  SumArgs m;
+  uint32_t per;         // pieces a workgroup adds
+  uint32_t clear_each;  // rows a workgroup clears
+};
+
+constexpr uint32_t kAlone = 8;
+
+// ROUNDS: tokens a lane compares.
+template <int DT, int GT, int VE, int ROUNDS>
+__global__ __launch_bounds__(256) void embed_few_kernel(FewArgs a) {
+  typedef Pack<DT, VE> K;
+  constexpr uint32_t kMost = ROUNDS * 256;
+  __shared__ uint32_t before[64], list[kMost];
+  __shared__ uint64_t masks[ROUNDS * 4];
+  __shared__ float parts[4][VE][64];
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const SumArgs& m = a.m;
+  rank_starts(a.t, before);
+  uint32_t key[ROUNDS], place[ROUNDS];
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const uint32_t i = r * 256 + threadIdx.x;
+    key[r] = m.vocab;
+    place[r] = 0;
+    if (i < m.total) key[r] = token_key(a.t, before, i, &place[r]);
+  }
+  if (blockIdx.x >= m.sum_groups) {
+    // list[x]: row `first + x` of the rank has a token
+    const uint32_t each = a.clear_each, units = (m.seg + each - 1) / each;
+    const uint32_t unit = blockIdx.x - m.sum_groups, rank = unit / units, first = (unit - rank * units) * each;
+    const uint32_t base = rank * m.seg;  // may pass the vocabulary's end on a rank that owns nothing
+    const uint32_t rows = base >= m.vocab ? 0 : min(m.seg, m.vocab - base);
+    const uint32_t n = first >= rows ? 0 : min(each, rows - first);
+    if (threadIdx.x < each) list[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      const uint32_t x = key[r] - (base + first);  // wraps for rows before
+      if (key[r] < m.vocab && x < n) list[x] = 1;
+    }
+    __syncthreads();
+    constexpr int GE = VE == 1 ? 1 : 16 / Width<GT>::bytes;
+    typedef Pack<GT, GE> Z;
+    const uint32_t vectors = (m.width + GE - 1) / GE;
+    unsigned char* to = m.out[rank] + uint64_t(first) * m.width * Z::E;
+    if (vectors >= 64) {
+      for (uint32_t x = wave; x < n; x += 4) {
+        if (uniform(list[x])) continue;
+        for (uint32_t v = lane; v < vectors; v += 64)
+          Z::store(to + (uint64_t(x) * m.width + Column<GE>(v, m.width).at) * Z::E, typename Z::raw{});
+      }
+    } else {
+      for (uint32_t v = threadIdx.x; v < n * vectors; v += 256) {
+        const uint32_t x = v / vectors;
+        if (!list[x]) Z::store(to + (uint64_t(x) * m.width + Column<GE>(v - x * vectors, m.width).at) * Z::E, typename Z::raw{});
+      }
+    }
+    return;
+  }
+  const uint32_t pieces = (m.width + VE * 64 - 1) / (VE * 64), shares = (pieces + a.per - 1) / a.per;
+  const uint32_t token = blockIdx.x / shares, from = (blockIdx.x - token * shares) * a.per;
+  uint32_t own_place;
+  const uint32_t own = uniform(token_key(a.t, before, token, &own_place));
+  if (own >= m.vocab) return;
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const uint64_t same = __ballot(key[r] == own);
+    if (lane == 0) masks[r * 4 + wave] = same;
+  }
+  __syncthreads();
+  uint32_t n = 0, at[ROUNDS];  // tokens of the id; of those, before this wave's r-th 64
+  bool leads = true;
+#pragma unroll
+  for (uint32_t k = 0; k < ROUNDS * 4; ++k) {
+    const uint64_t same = uniform(masks[k]);
+    if (k % 4 == wave) at[k / 4] = n;
+    if (n == 0 && same != 0) leads = k * 64 + __builtin_ctzll(same) == token;
+    n += __popcll(same);
+  }
+  if (!leads) return;
+#pragma unroll
+  for (int r = 0; r < ROUNDS; ++r) {
+    const uint64_t same = __ballot(key[r] == own);
+    if (key[r] == own) list[at[r] + __popcll(same & ((uint64_t(1) << lane) - 1))] = place[r];
+  }
+  __syncthreads();
+  // the lo-th to the hi-th of the id's tokens
+  const auto add = [&](const Column<VE>& c, uint32_t lo, uint32_t hi, float (&acc)[VE]) {
+    constexpr uint32_t U = kAlone;
+    for (uint32_t t = lo; t < hi; t += U) {
+      typename K::raw v[U];
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) {
+        if (t + u >= hi) continue;
+        const uint32_t pl = uniform(list[t + u]);
+        v[u] = K::load(m.rows[pl >> kPlaceBits] + (uint64_t(pl & ((1u << kPlaceBits) - 1)) * m.width + c.at) * K::E);
+      }
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) {
+        if (t + u >= hi) continue;
+        float f[VE];
+        K::widen(v[u], f);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[i] += f[i];
+      }
+    }
+  };
+  if (n <= kAlone * a.per) {
+    if (wave >= a.per || from + wave >= pieces) return;
+    const Column<VE> c((from + wave) * 64 + lane, m.width);
+    float old[VE] = {}, acc[VE] = {};
+    if (m.accumulate) load_row<GT, VE>(grad_at<GT>(m, own, c.at), old);
+    add(c, 0, n, acc);
+    write_row<GT, VE>(m, own, c, acc, old);
+    return;
+  }
+  const uint32_t each = (n + 3) / 4, lo = wave * each, hi = min(n, lo + each);
+  for (uint32_t piece = from; piece < min(from + a.per, pieces); ++piece) {
+    const Column<VE> c(piece * 64 + lane, m.width);
+    float old[VE] = {}, acc[VE] = {};
+    if (wave == 0 && m.accumulate) load_row<GT, VE>(grad_at<GT>(m, own, c.at), old);
+    add(c, lo, hi, acc);
+    __syncthreads();  // the piece before is joined
+#pragma unroll
+    for (int i = 0; i < VE; ++i) parts[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave != 0) continue;
+#pragma unroll
+    for (int w = 1; w < 4; ++w)
+#pragma unroll
+      for (int i = 0; i < VE; ++i) acc[i] += parts[w][i][lane];
+    write_row<GT, VE>(m, own, c, acc, old);
+  }
+}
+
 }  // namespace dev
 
 namespace {
@@ -569,6 +719,14 @@ constexpr uint32_t kMaxChunk = 64;  // a lane holds each token's pair
 // Tokens that one workgroup sorts by itself, in 8 us (1024) to 26 us (8192); the
 // four launches of the other way take 24 us for 16384.
 constexpr uint32_t kSingleTile = 8192;
+// Tokens that are added without sorting, in us beside the sort's way (8 ranks, bf16
+// into fp32, added): 1024 of 256 9.0 and 20; 1024 of 4096 20.7 and 22; the time
+// grows with the square of the tokens from there.
+constexpr uint32_t kFewTokens = 1024;
+// Of those, the pieces of rows up to which a workgroup takes one and not four:
+// 512 tokens of 2048 (2048 pieces) 8.2 us with one and 11.6 with four, 1024 of 2048
+// (4096) 17.5 and 18.2, 512 of 8192 (8192) 21 and 14.5.
+constexpr uint32_t kFewPieces = 4096;
 
 template <typename F>
 hipError_t with_rounds(uint32_t rounds, F&& f) {
@@ -602,11 +760,14 @@ hipError_t launch_embed(int dtype, const EmbedArgs& a, hipStream_t stream) {
 EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint64_t width) {
   EmbedGradSplit d;
   d.total = total;
+  const uint64_t pieces = (width + vector_elems(dtype, width) * 64 - 1) / (vector_elems(dtype, width) * 64);
+  d.few = total > 0 && total <= kFewTokens && pieces <= 4096;  // at most 2^20 workgroups
+  if (d.few) return d;
   uint32_t bits = 0;  // of the largest key, vocab itself
   while (vocab >> bits) ++bits;
   d.passes = (bits + 9) / 10;
   d.bits = (bits + d.passes - 1) / d.passes;
-  // pairs a thread sorts: one workgroup for few tokens, else 64 of them while
+  // pairs a thread sorts: one workgroup up to kSingleTile tokens, else 64 of them while
   // eight pairs a thread are enough
   d.rounds = 1;
   while (d.rounds < 8 && total > uint64_t(1024) * d.rounds * (total <= kSingleTile ? 1 : 64)) d.rounds *= 2;
@@ -621,7 +782,6 @@ EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint6
   // the waves are few; more of them leave fewer sums to join.  8 ranks, bf16 into
   // fp32, added: 4096 tokens of 1024 with 8 and 16 29 and 31.5 us; 32768 of 1024 65
   // and 59; 131072 of 512 with 16, 32 and 64 94, 86 and 93.
-  const uint64_t pieces = (width + vector_elems(dtype, width) * 64 - 1) / (vector_elems(dtype, width) * 64);
   d.chunk = total <= kSingleTile ? 8 : 16;
   while (d.chunk < kMaxChunk && (total * pieces / d.chunk > 8192 || total / d.chunk > 4096)) d.chunk *= 2;
   d.chunks = static_cast<uint32_t>((total + d.chunk - 1) / d.chunk);
@@ -642,17 +802,54 @@ EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint6
   return d;
 }
 
+namespace {
+
+// A call of few tokens (embed_few_kernel).
+hipError_t launch_few(int dtype, int grad_dtype, const SortArgs& s, const SumArgs& m, hipStream_t stream) {
+  FewArgs a = {s, m, 1, 0};
+  uint64_t clear = 0;
+  if (!m.accumulate) {
+    // 64 KiB a workgroup, or a row where that is more
+    const uint64_t row = uint64_t(m.width) * (grad_dtype == kF32 ? 4 : 2);
+    a.clear_each = static_cast<uint32_t>(std::clamp<uint64_t>(65536 / row, 1, 256));
+    clear = uint64_t(s.P) * ((m.seg + a.clear_each - 1) / a.clear_each);
+  }
+  return with_type(dtype, m.width, [&](auto dt, auto ve) {
+    const uint32_t pieces = (m.width + ve * 64 - 1) / (ve * 64);
+    a.per = m.total * pieces <= kFewPieces ? 1 : 4;
+    a.m.sum_groups = m.total * ((pieces + a.per - 1) / a.per);
+    const bool wide = grad_dtype == kF32 && dt != kF32;
+    void* argv[] = {&a};
+    return with_rounds(m.total <= 256 ? 1 : m.total <= 512 ? 2 : 4, [&](auto r) {
+      if constexpr (r > 4) return hipErrorInvalidValue;
+      else return go(wide ? reinterpret_cast<const void*>(&embed_few_kernel<dt, kF32, ve, r>)
+                          : reinterpret_cast<const void*>(&embed_few_kernel<dt, dt, ve, r>),
+                     a.m.sum_groups + clear, 256, argv, stream);
+    });
+  });
+}
+
+}  // namespace
+
 hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, const EmbedGradSplit& d, bool accumulate,
                              unsigned char* workspace, hipStream_t stream) {
   SortArgs s = {};
+  SumArgs m = {};
   for (int r = 0; r < a.P; ++r) {
     s.ids[r] = a.ids[r];
     s.tokens[r] = a.tokens[r];
+    m.rows[r] = a.rows[r];
+    m.out[r] = a.out[r];
   }
   s.P = a.P;
   s.id_bytes = a.id_bytes;
-  s.vocab = a.vocab;
-  s.total = static_cast<uint32_t>(d.total);
+  s.vocab = m.vocab = a.vocab;
+  s.total = m.total = static_cast<uint32_t>(d.total);
+  m.seg = a.seg;
+  m.width = a.width;
+  m.scale = a.scale;
+  m.accumulate = accumulate;
+  if (d.few) return launch_few(dtype, grad_dtype, s, m, stream);
   s.tiles = d.tiles;
   s.bits = d.bits;
   s.passes = d.passes;
@@ -704,23 +901,12 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
     });
   }
   if (e != hipSuccess) return e;
-  SumArgs m = {};
-  for (int r = 0; r < a.P; ++r) {
-    m.rows[r] = a.rows[r];
-    m.out[r] = a.out[r];
-  }
-  m.seg = a.seg;
-  m.vocab = a.vocab;
-  m.width = a.width;
-  m.total = s.total;
   m.chunk = d.chunk;
   m.chunks = d.chunks;
-  m.scale = a.scale;
   const int sorted = d.tiles <= 1 ? 0 : (d.passes - 1) & 1;
   m.key = s.key[sorted];
   m.place = s.place[sorted];
   m.touched = s.touched;
-  m.accumulate = accumulate;
   m.partial = reinterpret_cast<float*>(workspace + d.partial);
   return with_type(dtype, a.width, [&](auto dt, auto ve) {
     const uint64_t pieces = (a.width + ve * 64 - 1) / (ve * 64);

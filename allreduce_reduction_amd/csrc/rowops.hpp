@@ -102,6 +102,7 @@ struct EmbedGradSplit {
   uint32_t bits = 0, passes = 0;
   uint32_t chunk = 0, chunks = 0;  // sorted tokens a wave adds up
   bool clear_all = false;          // clear every row, not only those without a token
+  bool few = false;                // one launch, without sorting
   uint64_t key_a = 0, key_b = 0, place_a = 0, place_b = 0, hist = 0, touched = 0, partial = 0;  // byte offsets
   uint64_t bytes = 0;
 };

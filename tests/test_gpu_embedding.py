@@ -3,8 +3,9 @@ gradient) on the GPU against the formulas in 64 bits.
 
 Bounds: the lookup is one product, rounded to 32 bits and then to its type.
 The gradient of an id with m tokens adds them one after another in chunks of
-8 to 64 and then the chunks: below m + 2 additions, one product with scale
-and one addition where it accumulates: m + 4 roundings.
+8 to 64 and then the chunks (in calls of up to 1024 tokens all of them, or
+quarters of them and then these): below m + 2 additions, one product with
+scale and one addition where it accumulates: m + 4 roundings.
 """
 import pytest
 import torch
@@ -129,6 +130,27 @@ def test_sorting(N, vocab, H, kind, accumulate):
     chunks, cross them, and do not occur at all."""
     counts = [N // 3, N // 2, N - N // 3 - N // 2]
     gradient(3, counts, vocab, H, "bf16", "fp32", accumulate, kind, torch.int32)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("kind", ["skew", "one", "none", "runs", "even"])
+@pytest.mark.parametrize("N,vocab,H", [(1, 1, 1), (2, 3, 600), (9, 1, 520), (63, 20, 24), (64, 1000, 7), (65, 65, 1001), (255, 9, 2050),
+                                       (256, 70000, 4), (257, 3, 4099), (512, 300, 24), (513, 31, 6000), (768, 40, 2048), (1024, 77, 2600),
+                                       (1024, 30000, 64), (3000, 500, 136)])
+def test_few_tokens(N, vocab, H, kind, accumulate):
+    """Up to 1024 tokens take one launch without sorting: one, two and four
+    tokens a lane, one piece of a row a workgroup and four, ids of one wave and
+    of all four."""
+    counts = [N // 4, 0, N - N // 4 - N // 8, N // 8, 0]
+    gradient(5, counts, vocab, H, "bf16", "fp32", accumulate, kind, torch.int32)
+    gradient(5, counts, vocab, H, "fp16", "fp16", accumulate, kind, scale=-1.5, shift=1)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("H", [1048576, 1048577])
+def test_few_wide_rows(H, accumulate):
+    """Rows of up to 4096 pieces are added without sorting, wider ones with."""
+    gradient(2, [2, 1], 3, H, "fp32", "fp32", accumulate, "even")
 
 
 def test_gradient_alignment():

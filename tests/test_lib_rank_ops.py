@@ -156,12 +156,15 @@ def test_embedding_buffers(comm):
     assert emb_grad_call(comm, e, table=ptrs(4, BASE + (1 << 20), 1 << 20)) == BAD
     assert emb_grad_call(comm, e, table=ptrs(4, BASE + (16 << 20), 25 * 64 * 2)) == BAD  # overlap in fp32
     need = ctypes.c_size_t()
-    t = (ctypes.c_size_t * 4)(4, 4, 4, 4)
-    assert L.hbmc_embedding_grad_workspace(comm._h, e, t, ctypes.byref(need)) == OK
+    few = (ctypes.c_size_t * 4)(256, 256, 256, 256)  # needs none
+    assert L.hbmc_embedding_grad_workspace(comm._h, e, few, ctypes.byref(need)) == OK and need.value == 0
+    many = (400, 0, 400, 400)
+    t = (ctypes.c_size_t * 4)(*many)
+    assert L.hbmc_embedding_grad_workspace(comm._h, e, t, ctypes.byref(need)) == OK and need.value > 0
     assert L.hbmc_embedding_grad_workspace(comm._h, e, t, None) == BAD
     assert L.hbmc_embedding_grad_workspace(comm._h, e, None, ctypes.byref(need)) == BAD
-    assert emb_grad_call(comm, e, bytes_=need.value - 1) == BAD
-    assert emb_grad_call(comm, e, ws=None) == BAD and emb_grad_call(comm, e, ws=BASE + (1 << 31) + 8) == BAD
+    assert emb_grad_call(comm, e, many, bytes_=need.value - 1) == BAD
+    assert emb_grad_call(comm, e, many, ws=None) == BAD and emb_grad_call(comm, e, many, ws=BASE + (1 << 31) + 8) == BAD
     assert emb_grad_call(comm, e, (0, 0, 0, 0), acc=1, table=ptrs(4, BASE + (16 << 20), 1 << 20)) == OK  # nothing to add
 
 
