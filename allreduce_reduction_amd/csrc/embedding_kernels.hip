@@ -276,14 +276,27 @@ __global__ __launch_bounds__(1024) void embed_sort_kernel(SortArgs a, uint32_t p
       }
     }
   }
-  // the tiles' counts, on their way while the pairs are ranked
-  uint32_t all = 0, prior = 0;
+  // The tiles' counts, on their way while the pairs are ranked: 16 at once, the
+  // last ones too (one after another they took 2 us of the launch's 9 for 12 tiles).
+  uint32_t all = 0, prior = 0, t = 0;
   const uint32_t* h = a.hist + threadIdx.x;
-#pragma unroll 16
-  for (uint32_t t = 0; t < a.tiles; ++t) {
-    const uint32_t c = h[t * kMaxBins];
-    all += c;
-    prior += t < blockIdx.x ? c : 0;
+  for (; t + 16 <= a.tiles; t += 16) {
+#pragma unroll
+    for (uint32_t k = 0; k < 16; ++k) {
+      const uint32_t c = h[(t + k) * kMaxBins];
+      all += c;
+      prior += t + k < blockIdx.x ? c : 0;
+    }
+  }
+  if (t < a.tiles) {
+    uint32_t c[16];
+#pragma unroll
+    for (uint32_t k = 0; k < 16; ++k) c[k] = h[min(t + k, a.tiles - 1) * kMaxBins];
+#pragma unroll
+    for (uint32_t k = 0; k < 16; ++k) {
+      all += t + k < a.tiles ? c[k] : 0;
+      prior += t + k < blockIdx.x ? c[k] : 0;
+    }
   }
   sort_positions<R>(key, on, pass * a.bits, a.bits, count, scan, [&](uint32_t* x, uint32_t* y) { *x = all, *y = prior; }, to);
   if (pass == 0) mark<R>(a, key, on);
