@@ -4,8 +4,10 @@
 //   s = sum of the ranks' rows        r1 = 1 / rms(s)     n = s * r1 * w1
 //   h = residual + scale * gate * n   r2 = 1 / rms(h)     out = h * r2 * w2
 // and back, with g the sum of the ranks' gradients and a = g * w2,
-//   dh = r2 * a - h * r2^3 * mean(a * h) + dresidual_out
-//   b = scale * gate * w1 * dh        ds = r1 * b - s * r1^3 * mean(b * s)
+//   u = h * r2                        dh = r2 * (a - u * mean(a * u)) + dresidual_out
+//   b = scale * gate * w1 * dh        v = s * r1    ds = r1 * (b - v * mean(b * v))
+// (mean(a * u) is r2 * mean(a * h): no power of r1 or r2, which would leave
+// fp32's range long before the rows' squares do.)
 //
 // Both directions stream: a row is P operand rows in, P copies out and a few
 // rows of one rank, each touched once, with every row statistic taken from
@@ -361,7 +363,7 @@ __global__ __launch_bounds__(GradTile<WAVES>::kGroup) void norm_grad_kernel(Norm
     }
     row_sums<WAVES, R::kSlots>(q, red, slot, wave, &turn);
     const float r2 = 1.0f / sqrtf(q[0] * inv + s.pre_eps);
-    const float c2 = r2 * r2 * r2 * (q[1] * inv);
+    const float c2 = r2 * (q[1] * inv);
     const float r1 = w1p ? 1.0f / sqrtf(q[2] * inv + s.post_eps) : 1.0f;
     // g becomes the gradient of the hidden row, then of the norm's output
     float inner[1] = {0.0f};
@@ -388,12 +390,12 @@ __global__ __launch_bounds__(GradTile<WAVES>::kGroup) void norm_grad_kernel(Norm
       if (active) {
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
-          if constexpr (R::kWide) held[0][slot_of(k, i)] += g[k][i] * h[i] * r2;
-          else d2[j][i] += g[k][i] * h[i] * r2;
+          if constexpr (R::kWide) held[0][slot_of(k, i)] += g[k][i] * (h[i] * r2);
+          else d2[j][i] += g[k][i] * (h[i] * r2);
         }
       }
 #pragma unroll
-      for (int i = 0; i < VE; ++i) g[k][i] = r2 * (g[k][i] * w[i]) - h[i] * c2 + in[i];
+      for (int i = 0; i < VE; ++i) g[k][i] = r2 * (g[k][i] * w[i] - h[i] * r2 * c2) + in[i];
       if (active && lane.on[k]) K::store(a.residual_out[owner] + local + b, K::narrow(g[k]));
 #pragma unroll
       for (int i = 0; i < VE; ++i) g[k][i] *= s.scale;
@@ -418,7 +420,7 @@ __global__ __launch_bounds__(GradTile<WAVES>::kGroup) void norm_grad_kernel(Norm
     }
     if (w1p) {
       row_sums<WAVES, R::kSlots>(inner, red, slot, wave, &turn);
-      const float c1 = r1 * r1 * r1 * (inner[0] * inv);
+      const float c1 = r1 * (inner[0] * inv);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int j = R::kWide ? 0 : k;
@@ -430,7 +432,7 @@ __global__ __launch_bounds__(GradTile<WAVES>::kGroup) void norm_grad_kernel(Norm
         float x[VE];
         K::widen(sr[j], x);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) g[k][i] = r1 * g[k][i] - x[i] * c1;
+        for (int i = 0; i < VE; ++i) g[k][i] = r1 * (g[k][i] - x[i] * r1 * c1);
       }
     }
     if (active) {

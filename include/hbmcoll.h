@@ -533,8 +533,9 @@ hbmc_status_t hbmc_graph_destroy(hbmc_graph_t graph);
  *   n = s / sqrt(mean(s^2) + post_eps) * post_weight    (s without post_weight)
  *   h = residual[t] + scale * gate[t / gate_rows] * n   (no gate: 1)
  *   out[p][t] = h / sqrt(mean(h^2) + pre_eps) * pre_weight, on every rank p
- * with every intermediate in 32 bits (a row whose squares add up past 3.4e38
- * has no norm).  gate has ceil(rows / gate_rows) rows.
+ * with every intermediate in 32 bits (a row whose squares add up past 3.4e38,
+ * or with an eps of 0 to nothing, has no norm).  gate has ceil(rows /
+ * gate_rows) rows.
  */
 typedef struct {
   size_t rows, width;

@@ -256,3 +256,27 @@ def test_gradient_against_differences():
         # differences: step^2 of the third derivative and 2^-52 / step of the
         # loss; gradient: 123 + 56 roundings of terms up to a few times its own
         assert abs(diff - along) <= 1e-4 * size + 1e-6, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H", [64, 1000, 16384])
+@pytest.mark.parametrize("hidden,sums,eps", [(1e15, 1.0, 1e-6), (1.0, 1e15, 1e-6), (1e16, 1e16, 1e-6), (1e-14, 1e-14, 0.0),
+                                             (1e-17, 1.0, 0.0), (1.0, 1e-17, 0.0), (1e-14, 1e-14, 1e-30)])
+def test_rows_of_any_size(hidden, sums, eps, H, dtype):
+    """Rows whose size's cube, or its inverse, leaves fp32's range: the
+    gradient is bounded as everywhere else.  (Squares of 1e16 add up to 2e36
+    over 16384 columns; gradients stay between 1e-33 and 1e35.)  A tiny eps
+    takes a row of zeros too, whose gradient is the incoming one over its
+    root."""
+    c = case(3, 6, H, dtype, True, 2)
+    x = c["parts"].double().sum(0)
+    c["residual"] = (c["residual"].double() / 2 * hidden).to(TYPES[dtype])
+    # the gradient's sums are the rounded sum over the ranks of `parts`
+    c["parts"] = torch.stack([(x * sums).to(TYPES[dtype]), torch.zeros_like(c["parts"][0]), torch.zeros_like(c["parts"][0])])
+    if eps == 1e-30:
+        c["residual"][2], c["parts"][:, 2] = 0, 0
+    with hc.Comm(3, "ring") as comm:
+        got, want = backward(c, comm, has_in=False, eps=eps)
+        assert all(bool(torch.isfinite(v).all()) for v, _ in want.values())
+        check_backward(got, want)
+        check_forward(forward(c, comm, eps=eps), c, eps=eps)
