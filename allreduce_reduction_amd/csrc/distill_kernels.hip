@@ -40,14 +40,14 @@ __device__ __forceinline__ int64_t teacher_id(const DistillArgs& a, uint64_t i) 
 }
 
 // The i-th teacher entry: its column (vocab where it does not count) and its
-// logit over the temperature.
+// logit.
 __device__ __forceinline__ uint32_t teacher_entry(const DistillArgs& a, uint64_t i, float* t) {
   const int64_t id = teacher_id(a, i);
   float f[1];
   if (a.teacher_dtype == kF32) Pack<kF32, 1>::widen(Pack<kF32, 1>::load(a.teacher + i * 4), f);
   else if (a.teacher_dtype == kF16) Pack<kF16, 1>::widen(Pack<kF16, 1>::load(a.teacher + i * 2), f);
   else Pack<kBF16, 1>::widen(Pack<kBF16, 1>::load(a.teacher + i * 2), f);
-  *t = f[0] * (1.0f / a.temperature);
+  *t = f[0];
   return id >= 0 && id < static_cast<int64_t>(a.vocab) && f[0] != -__builtin_inff() ? static_cast<uint32_t>(id) : a.vocab;
 }
 
@@ -68,7 +68,7 @@ struct Teacher {
       if (h * 64 + lane < a.top) col[h] = teacher_entry(a, row * a.top + h * 64 + lane, &t[h]);
     }
   }
-  // f(entry's logit / temperature, column) for the lane's entries that count.
+  // f(entry's logit, column) for the lane's entries that count.
   template <typename F>
   __device__ __forceinline__ void each(const DistillArgs& a, uint64_t row, uint32_t lane, F&& f) const {
 #pragma unroll
@@ -80,7 +80,10 @@ struct Teacher {
       if (c < a.vocab) f(x, c);
     }
   }
-  // Fills top and sum; false where no entry counts.
+  // Fills top and sum; false where no entry counts.  The differences to the
+  // largest entry are taken before the factor 1 / temperature: above 1 it would
+  // take entries at the type's lowest or largest value past fp32's range, and a
+  // row of them alone has differences of zero.
   __device__ __forceinline__ bool stats(const DistillArgs& a, uint64_t row, uint32_t lane) {
     float m = -__builtin_inff(), s = 0.0f;
     bool any = false;
@@ -90,7 +93,8 @@ struct Teacher {
     });
     if (__ballot(any) == 0) return false;
     top = wave_max(m);
-    each(a, row, lane, [&](float x, uint32_t) { s += exp_fast(x - top); });
+    const float inv = 1.0f / a.temperature;
+    each(a, row, lane, [&](float x, uint32_t) { s += exp_fast((x - top) * inv); });
     sum = wave_sum(s);
     return true;
   }
@@ -243,9 +247,9 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, uint64_t row, u
   if (e.stats(a, row, lane)) {
     const float log_sum = logf(e.sum), inv_sum = 1.0f / e.sum;
     const auto add = [&](float t, float logit) {
-      const float q = exp_fast(t - e.top) * inv_sum;
+      const float far = (t - e.top) * inv, q = exp_fast(far) * inv_sum;
       const float log_p = lse == -__builtin_inff() ? lse : logit * inv - lse;
-      const float term = q * ((t - e.top) - log_sum - log_p);
+      const float term = q * (far - log_sum - log_p);
       loss += q == 0.0f ? 0.0f : term;
     };
 #pragma unroll
@@ -370,7 +374,7 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
     if (in) {
       Entry& e = list[n + __popcll(who & ((uint64_t(1) << lane) - 1))];
       e.col = col - lo;
-      e.q = exp_fast(t - teach.top) * inv_sum;
+      e.q = exp_fast((t - teach.top) * inv) * inv_sum;
     }
     n += __popcll(who);
   }

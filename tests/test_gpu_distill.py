@@ -161,3 +161,56 @@ def test_gradient_against_differences():
     along = (grads.double().cpu() * way).sum()
     size = (grads.double().cpu() * way).abs().sum()
     assert abs((diff - along).item()) <= 1e-4 * size.item() + 1e-6
+
+
+def check_far(z, t, ids, dl, P, tau):
+    """Teacher rows of any size: q follows from differences to the row's
+    largest counting entry, and one that is not zero lies within 104 / 1 of it
+    (exp(-104) is below fp32's smallest number), so its roundings count 104 in
+    the place of the entries' own size."""
+    loss, lse, grads = run(z, t, ids, dl, P, tau)
+    zz = z.double() / tau
+    want_lse = torch.logsumexp(zz, 1)
+    ref.check(lse, (want_lse, want_lse.abs() + zz.abs().max(1).values), 100, "lse")
+    q, log_q, some = ref.teacher(t, ids, z.shape[1], tau)
+    at = ids.long().clamp(0, z.shape[1] - 1)
+    log_p = zz.gather(1, at) - want_lse[:, None]
+    size = zz.abs().max(1).values + want_lse.abs()
+    on = q > 1e-44
+    terms = torch.where(on, q * (log_q - log_p), 0.0)
+    mag = torch.where(on, q * (log_q.abs() + log_p.abs() + 104 + size[:, None]), 0.0)
+    ref.check(loss, (tau * tau * terms.sum(1), tau * tau * mag.sum(1)), 140, "loss")
+    p = (zz - lse.double().cpu()[:, None]).exp()
+    by = (dl.double() * tau)[:, None]
+    value = p.scatter_add(1, at, -q) * by * some[:, None]
+    # p and q below fp32's normal range are multiples of 2^-149, each off by up
+    # to 2^-150, before the product with `by` is rounded there once more
+    small = 2 * 2.0 ** -150 / (40 * 2.0 ** -24)
+    mag = (small + p * (1 + size[:, None]) + torch.zeros_like(p).scatter_add(1, at, q * 105)) * by.abs() * some[:, None]
+    ref.check(grads, (value, mag), 40, "grads")
+
+
+@pytest.mark.parametrize("tau", [0.25, 0.5, 1.0, 3.0])
+@pytest.mark.parametrize("tdtype", ["bf16", "fp32", "fp16"])
+@pytest.mark.parametrize("rows,k", [(12, 16), (12, 300), (600, 16)])
+def test_teacher_rows_of_any_size(rows, k, tdtype, tau):
+    """Entries masked by the type's lowest value count, alone in their row or
+    beside others, and so do entries near its largest one; their quotients by
+    a temperature below 1 lie past the type's range."""
+    z, t, ids, dl = case(rows, 9000, k, "fp32", tdtype, seed=6)
+    top, low = torch.finfo(TYPES[tdtype]).max, torch.finfo(TYPES[tdtype]).min
+    t[0] = low
+    t[1, 1:] = low
+    t[2] = top
+    t[3, :k // 2] = top
+    t[4, 3] = 0.8 * top
+    t[5] = low
+    ids[5, 1:] = -1  # one counting entry
+    t[6] = low
+    ids[6] = ids[6, 0]  # one column
+    t[7, ::2], t[7, 1::2] = low, -torch.inf
+    t[8] = 0.9 * low
+    t[8, k - 1] = low
+    t[9] = top
+    t[9, 0] = low
+    check_far(z, t, ids, dl, 4, tau)
