@@ -242,13 +242,15 @@ __device__ __forceinline__ void finish_row(const DistillArgs& a, uint64_t row, u
   for (uint32_t i = lane; i < parts; i += 64)
     s += part[i].y * expf((part[i].x == -__builtin_inff() ? 0.0f : part[i].x - base) * inv);
   s = wave_sum(s);
-  const float lse = base * inv + logf(s);
+  const float log_s = logf(s), lse = base * inv + log_s;
   float loss = 0.0f;
   if (e.stats(a, row, lane)) {
     const float log_sum = logf(e.sum), inv_sum = 1.0f / e.sum;
     const auto add = [&](float t, float logit) {
       const float far = (t - e.top) * inv, q = exp_fast(far) * inv_sum;
-      const float log_p = lse == -__builtin_inff() ? lse : logit * inv - lse;
+      // from the difference to the row's maximum: base * inv and with it lse may
+      // lie past fp32's range.  s is zero for a row of -infinity alone.
+      const float log_p = s == 0.0f ? -__builtin_inff() : (logit - base) * inv - log_s;
       const float term = q * (far - log_sum - log_p);
       loss += q == 0.0f ? 0.0f : term;
     };

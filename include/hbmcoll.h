@@ -625,7 +625,9 @@ typedef struct {
 
 /* Writes loss [rows] and lse [rows], log sum_j exp(logits_j / temperature).
  * A row whose logits are all -infinity has lse -infinity and, where an entry
- * counts, loss +infinity; a NaN or +infinity among its logits gives NaN. */
+ * counts, loss +infinity; a NaN or +infinity among its logits gives NaN.  Where
+ * finite logits over a temperature below 1 pass fp32's range lse is an infinity,
+ * while the loss, taken from differences of logits, stays the formula's. */
 hbmc_status_t hbmc_distill_loss_workspace(hbmc_comm_t comm, const hbmc_distill_t* distill, size_t* bytes);
 hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
                                 float* loss, float* lse, void* workspace, size_t workspace_bytes, void* stream);
@@ -633,9 +635,10 @@ hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill,
 /* logit_grads[r][t][j] = loss_grad[t] * temperature * (p_j - the sum of q_k
  * over the entries with column j), from the forward call's lse; zeros for a
  * row whose loss_grad is zero or that has no counting entry, whatever its
- * logits hold; p is zero in a row whose lse is -infinity, and comes from lse as
- * it is, in 32 bits (a row that holds the type's lowest value alone has p = 1
- * throughout).  logit_grads[r] may be logits[r]. */
+ * logits hold; p is zero in a row whose lse is an infinity, and comes from lse
+ * as it is, in 32 bits: its relative error is |lse| * 2^-24 and more, so that a
+ * row that holds fp32's or bf16's lowest value alone has p = 1 throughout (at
+ * temperatures below 1: 0).  logit_grads[r] may be logits[r]. */
 hbmc_status_t hbmc_distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
                                      const float* lse, const float* loss_grad, void* const logit_grads[],
                                      void* stream);

@@ -214,3 +214,28 @@ def test_teacher_rows_of_any_size(rows, k, tdtype, tau):
     t[9] = top
     t[9, 0] = low
     check_far(z, t, ids, dl, 4, tau)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows", [4, 520])
+def test_student_rows_past_the_range(rows, dtype):
+    """Logits whose quotient by a temperature below 1 lies past fp32's range:
+    the log-sum-exp is then an infinity (and p zero in the gradient), but the
+    loss comes from differences.  8 entries, q known to 140 roundings of
+    magnitudes below 16."""
+    z, t, ids, dl = case(rows, 3000, 8, dtype, seed=3)
+    info = torch.finfo(TYPES[dtype])
+    z[0] = info.min  # uniform
+    z[1, ids[1]] = info.max  # uniform over the teacher's columns
+    tau = 0.5
+    loss, lse, grads = run(z, t, ids, dl, 3, tau)
+    q, log_q, _ = ref.teacher(t, ids, 3000, tau)
+    entropy = (q * log_q).sum(1)
+    for row, log_n in ((0, torch.tensor(3000.0).log()), (1, torch.tensor(8.0).log())):
+        want = tau * tau * (entropy[row] + log_n)
+        assert abs(loss[row].item() - want.item()) <= 140 * 2.0 ** -24 * 16, row
+    assert lse[0] == -torch.inf and lse[1] == torch.inf and torch.isfinite(lse[2:]).all()
+    assert torch.isfinite(loss).all() and not torch.isnan(grads).any()
+    want = torch.zeros(2, 3000).double().scatter_add(1, ids[:2], -q[:2]) * (dl[:2].double() * tau)[:, None]
+    mag = torch.zeros(2, 3000).double().scatter_add(1, ids[:2], 105 * q[:2]) * (dl[:2].double().abs() * tau)[:, None]
+    ref.check(grads[:2], (want, mag), 40, "grads")
