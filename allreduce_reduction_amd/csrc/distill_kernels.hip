@@ -22,7 +22,6 @@ namespace dev {
 // is stored.  8 ranks, bf16, 2048 x 131072: gradient with two, four and eight 187,
 // 169 and 183 us; loss of 2048 x 100277 with four, six and eight 73, 85 and 72.
 constexpr uint32_t kLossVectors = 8, kGradVectors = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int DT, uint32_t VECTORS>
 struct Piece {

@@ -270,8 +270,8 @@ hbmc_status_t distill_args(hbmc_comm_t comm, const hbmc_distill_t* m, bool grad,
     if (float_bytes(t) == 0) return t == HBMC_INT32 || t == HBMC_INT8 ? HBMC_ERR_UNSUPPORTED : HBMC_ERR_INVALID_ARG;
   uint64_t bytes;
   if (m->vocab == 0 || m->vocab > kMaxVocab || m->top == 0 || m->rows > kMaxRows || (m->id_bytes != 4 && m->id_bytes != 8) ||
-      !(m->temperature > 0.0f) || !finite(1.0f / m->temperature) || !finite(m->temperature * m->temperature) || !matrix_bytes(m->rows, m->vocab, 4, &bytes) ||
-      !matrix_bytes(m->rows, m->top, 8, &bytes))
+      !(m->temperature > 0.0f) || !finite(1.0f / m->temperature * kLog2e) || !finite(m->temperature * m->temperature) ||
+      !matrix_bytes(m->rows, m->vocab, 4, &bytes) || !matrix_bytes(m->rows, m->top, 8, &bytes))
     return HBMC_ERR_INVALID_ARG;
   if (m->top > kMaxTop) return HBMC_ERR_UNSUPPORTED;
   a->rows = m->rows;

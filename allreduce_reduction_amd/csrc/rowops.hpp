@@ -114,6 +114,7 @@ hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, cons
 // ------------------------------------------------------ distillation loss
 
 constexpr uint64_t kMaxTop = 1024;
+constexpr float kLog2e = 1.44269504088896340736f;  // the kernels' exponents: differences * (1 / temperature * kLog2e)
 
 struct DistillArgs {
   const unsigned char* logits[kMaxRanks];

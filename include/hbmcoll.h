@@ -618,7 +618,7 @@ typedef struct {
   hbmc_dtype_t dtype;         /* of the logits and their gradients             */
   hbmc_dtype_t teacher_dtype; /* fp32, fp16 or bf16                            */
   int id_bytes;               /* 4 or 8 (signed)                               */
-  float temperature;          /* > 0, its square and inverse finite in 32 bits */
+  float temperature;          /* 4.3e-39 to 1.8e19: its square and log2(e) / it are finite in 32 bits */
   const void* teacher_logits; /* [rows][top]                                   */
   const void* teacher_ids;    /* [rows][top]                                   */
 } hbmc_distill_t;

@@ -198,6 +198,16 @@ def test_distill_descriptor(comm, kw, code):
     assert distill_grad_call(comm, distill_args(**kw)) == code
 
 
+@pytest.mark.parametrize("temperature,code", [(1e-39, BAD), (2.95e-39, BAD), (4.2e-39, BAD), (4.3e-39, OK), (1e-30, OK), (1e19, OK),
+                                              (1.9e19, BAD)])
+def test_distill_temperatures(comm, temperature, code):
+    """The kernels multiply by log2(e) / temperature, which has to be finite."""
+    d = distill_args(rows=0, teacher_logits=None, teacher_ids=None, temperature=temperature)
+    assert distill_call(comm, d, loss=None, lse=None, ws=None, bytes_=0, logits=ptrs(4, 0, 0)) == code
+    assert distill_grad_call(comm, d, lse=None, dl=None, logits=ptrs(4, 0, 0), grads=ptrs(4, 0, 0)) == code
+    assert L.hbmc_distill_loss_workspace(comm._h, d, ctypes.byref(ctypes.c_size_t())) == code
+
+
 def test_distill_buffers(comm):
     d = distill_args()
     assert distill_call(comm, distill_args(rows=0, teacher_logits=None, teacher_ids=None), loss=None, lse=None, ws=None,
