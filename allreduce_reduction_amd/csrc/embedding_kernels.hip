@@ -770,10 +770,23 @@ hipError_t launch_embed(int dtype, const EmbedArgs& a, hipStream_t stream) {
   });
 }
 
+namespace {
+uint64_t row_pieces(int dtype, uint64_t width) {
+  const uint64_t piece = vector_elems(dtype, width) * 64;
+  return (width + piece - 1) / piece;
+}
+}  // namespace
+
+// The joining launch is the largest: fewer than tokens / 64 * pieces workgroups
+// of 256 threads there (kMaxChunk tokens a chunk in calls this large).
+bool embed_grad_fits(int dtype, uint64_t total, uint64_t width) {
+  return total * row_pieces(dtype, width) <= uint64_t(1) << 30;
+}
+
 EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint64_t width) {
   EmbedGradSplit d;
   d.total = total;
-  const uint64_t pieces = (width + vector_elems(dtype, width) * 64 - 1) / (vector_elems(dtype, width) * 64);
+  const uint64_t pieces = row_pieces(dtype, width);
   d.few = total > 0 && total <= kFewTokens && pieces <= 4096;  // at most 2^20 workgroups
   if (d.few) return d;
   uint32_t bits = 0;  // of the largest key, vocab itself

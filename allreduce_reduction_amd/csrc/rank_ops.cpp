@@ -243,6 +243,7 @@ hbmc_status_t embedding_grad(hbmc_comm_t comm, const hbmc_embedding_t* m, const 
   hbmc_status_t st = embed_args(comm, m, tokens, &a, &total);
   if (st != HBMC_OK) return st;
   if (!out_grads || !ids || !table_grads || (grad_dtype != HBMC_FP32 && grad_dtype != m->dtype)) return HBMC_ERR_INVALID_ARG;
+  if (!embed_grad_fits(m->dtype, total, a.width)) return HBMC_ERR_UNSUPPORTED;
   const EmbedGradSplit d = split_embed_grad(m->dtype, total, a.vocab, a.width);
   if (workspace_bytes < d.bytes) return HBMC_ERR_INVALID_ARG;
   const uint32_t e = float_bytes(m->dtype), ge = float_bytes(grad_dtype);
@@ -385,8 +386,10 @@ hbmc_status_t hbmc_embedding_grad_workspace(hbmc_comm_t comm, const hbmc_embeddi
     uint64_t total;
     if (!bytes) return HBMC_ERR_INVALID_ARG;
     const hbmc_status_t st = embed_args(comm, emb, tokens, &a, &total);
-    if (st == HBMC_OK) *bytes = split_embed_grad(emb->dtype, total, a.vocab, a.width).bytes;
-    return st;
+    if (st != HBMC_OK) return st;
+    if (!embed_grad_fits(emb->dtype, total, a.width)) return HBMC_ERR_UNSUPPORTED;
+    *bytes = split_embed_grad(emb->dtype, total, a.vocab, a.width).bytes;
+    return HBMC_OK;
   });
 }
 

@@ -107,6 +107,8 @@ struct EmbedGradSplit {
   uint64_t bytes = 0;
 };
 EmbedGradSplit split_embed_grad(int dtype, uint64_t total, uint64_t vocab, uint64_t width);
+// Whether every launch of the gradient stays below 2^32 threads.
+bool embed_grad_fits(int dtype, uint64_t total, uint64_t width);
 hipError_t launch_embed(int dtype, const EmbedArgs& a, hipStream_t stream);
 hipError_t launch_embed_grad(int dtype, int grad_dtype, const EmbedArgs& a, const EmbedGradSplit& d, bool accumulate,
                              unsigned char* workspace, hipStream_t stream);

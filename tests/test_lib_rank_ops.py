@@ -168,6 +168,26 @@ def test_embedding_buffers(comm):
     assert emb_grad_call(comm, e, (0, 0, 0, 0), acc=1, table=ptrs(4, BASE + (16 << 20), 1 << 20)) == OK  # nothing to add
 
 
+@pytest.mark.parametrize("width,dtype,pieces", [(1, 2, 1), (7, 1, 1), (512, 2, 1), (513, 2, 2), (1200, 1, 3), (1024, 0, 4),
+                                                (4096, 2, 8)])
+def test_embedding_gradient_limit(width, dtype, pieces):
+    """A launch takes fewer than 2^32 threads, and the joining one has 256 for
+    each 64 tokens and piece of a row (64 vectors of 16 bytes): tokens times
+    pieces past 2^30 are refused, before anything is launched."""
+    limit, need = 2 ** 30 // pieces, ctypes.c_size_t()
+    none = ptrs(64, 0, 0)
+    with hc.Comm(64, "ring") as c:
+        def counts(total):
+            return (ctypes.c_size_t * 64)(*[total // 64 + (r < total % 64) for r in range(64)])
+        e = emb_args(width=width, dtype=dtype)
+        assert L.hbmc_embedding_grad_workspace(c._h, e, counts(limit), ctypes.byref(need)) == OK and need.value > 16 * limit
+        assert (-(-limit // 64) - 1) * pieces < 2 ** 24
+        for total in (limit + 1, min(2 * limit, 2 ** 31 - 1)):
+            assert L.hbmc_embedding_grad_workspace(c._h, e, counts(total), ctypes.byref(need)) == UNSUPPORTED, total
+            assert L.hbmc_embedding_grad(c._h, e, none, none, counts(total), none, 0, 0, None, 0, None) == UNSUPPORTED, total
+            assert L.hbmc_embedding(c._h, e, none, none, counts(total), none, None) == BAD  # the lookup takes them: NULLs
+
+
 def distill_args(**kw):
     d = dict(rows=4, vocab=100, top=8, dtype=2, teacher_dtype=0, id_bytes=8, temperature=1.0, teacher_logits=BASE,
              teacher_ids=BASE + 65536)
