@@ -362,7 +362,7 @@ class Comm:
         dev = _current_device()
         if scratch:
             args += (lambda nbytes: _scratch(nbytes, dev, stream),)
-        rc = getattr(load_operators(), name)(self._h.value, self.P, dev, _stream(stream), *args)
+        rc = getattr(load_operators(), name)(self._h.value or 0, self.P, dev, _stream(stream), *args)
         if rc != OK:
             raise HbmcError(rc, "hbmc_" + name)
 

@@ -317,6 +317,16 @@ def test_binding_types(comm, on_device):
     assert e.value.code == BAD
 
 
+def test_closed_communicator(on_device):
+    """As with the collectives: the library's refusal, not a conversion's."""
+    c = hc.Comm(4, "ring")
+    c.close()
+    for call in (lambda: norm_binding(c), lambda: c.embedding(fakes(4, (5, 16)), fakes(4, (3,), dtype=torch.int64), fakes(4, (3, 16)))):
+        with pytest.raises(hc.HbmcError) as e:
+            call()
+        assert e.value.code == BAD
+
+
 def test_norm_gradient_binding_refuses(comm, on_device):
     def call(**kw):
         a = dict(out_grads=fakes(4, (8, 16)), hidden=fakes(4, (2, 16), 10), part_grads=fakes(4, (8, 16), 20),
