@@ -2,8 +2,8 @@
 // call, collects their addresses and calls the C ABI (include/hbmcoll.h).
 //
 // A decode step's operator runs for about 5 us, and a call names up to 40
-// tensors; checking each from Python costs 0.6 us a tensor (19 us for the norms
-// of 8 ranks), here some 20 ns.
+// tensors.  The norms' of 8 ranks: 28 us for the checks in Python and 1.5 us for
+// the whole call here, on one host; one row's call 19.1 and 5.6 us on an MI355X's.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>

@@ -52,8 +52,9 @@ __device__ __forceinline__ uint32_t teacher_entry(const DistillArgs& a, uint64_t
 
 // A row's teacher entries: a lane's first kHeld stay in registers, so that they
 // are read once; further ones are read where they are used.  (Gradient of 2048
-// x 50001 bf16 logits with 256 entries a row: 110 us with four held, 126 with
-// two, 115 with eight, 131 with 16; with 64 entries 93 us.)
+// x 50001 bf16 logits with 256 entries a row, when this was chosen: 110 us with
+// four held, 126 with two, 115 with eight, 131 with 16.  Now 95; with 64 entries
+// 78, with 1024 373.)
 constexpr uint32_t kHeld = 4;
 struct Teacher {
   float t[kHeld];

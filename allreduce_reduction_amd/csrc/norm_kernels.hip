@@ -684,7 +684,10 @@ NormGradSplit split_norm_grad(int dtype, const NormShape& s) {
   const uint32_t S = grad_slots(row_form(dtype, s.width, true, s.rows).waves);
   // One workgroup a compute unit: each more leaves a row of partial sums more
   // (4096 rows of 4096, 8 ranks, bf16: 139 us with 256, 149 with 384, 144 with
-  // 512, 152 with 1024 workgroups, 190 with 128).
+  // 512, 152 with 1024 workgroups, 190 with 128).  Fewer where gate groups are
+  // direct and longer than C / S rows: each slot takes at least a whole one
+  // (8192 rows of 512, 8 ranks, bf16: one gate row 38 us; 16 rows a gate, 64
+  // workgroups, 78; 32 rows, 32 workgroups, 123; 33 rows, not direct, 51).
   const uint32_t target = 256;
   const uint32_t C = up(std::max(up(s.rows, target), 1u), S) * S;  // rows a chunk
   const uint32_t R = s.gate_rows;

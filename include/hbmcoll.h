@@ -595,8 +595,9 @@ hbmc_status_t hbmc_embedding(hbmc_comm_t comm, const hbmc_embedding_t* emb, cons
  * with `accumulate` added to what table_grads holds, whose other rows are then
  * left untouched.  Without it every row is written, zeros where no token has
  * its id.  HBMC_ERR_UNSUPPORTED: tokens in all, times 1 KiB pieces of a row of
- * out_grads (1 for rows of up to 1 KiB), past 2^30.  Up to about a million tokens
- * the time grows with them, from there with their square. */
+ * out_grads (1 for rows of up to 1 KiB), past 2^30.  Up to some 4 million
+ * tokens the time grows with them, from there with their square (16 million take
+ * 4 ms, 64 million 56). */
 hbmc_status_t hbmc_embedding_grad_workspace(hbmc_comm_t comm, const hbmc_embedding_t* emb, const size_t tokens[],
                                             size_t* bytes);
 hbmc_status_t hbmc_embedding_grad(hbmc_comm_t comm, const hbmc_embedding_t* emb, const void* const out_grads[],
