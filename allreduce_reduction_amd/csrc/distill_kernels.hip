@@ -349,12 +349,14 @@ __device__ __forceinline__ void piece_grad(const DistillArgs& a, const Place& p,
     if (c.has_rest) K1::store(out + uint64_t(c.rest) * K::E, 0);
     return;
   }
-  // p, zero throughout where lse is -infinity.  The difference is taken before
-  // the factor log2 e: with logits at the type's lowest value either product
-  // alone would overflow.
-  const float shift = lse == -__builtin_inff() ? lse : -lse;
+  // p = exp(z / temperature - lse).  The quotient is rounded by itself, as it was
+  // for lse, so that the row's largest logit, however large, cancels: fused, the
+  // difference would hold its rounding error.  Zero throughout where lse is an
+  // infinity: z * FLT_MIN is finite or -infinity itself, of which that is taken.
+  const bool past = __builtin_isinf(lse);
+  const float scale = past ? __FLT_MIN__ : inv, shift = past ? -__builtin_inff() : -lse;
   const auto prob = [&](float z) {
-    const float x = __builtin_fmaf(z, inv, shift);
+    const float x = z * scale + shift;
     if constexpr (DT == kF32) return expf(x);
     else return exp_fast(x);
   };

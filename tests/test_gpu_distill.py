@@ -239,3 +239,30 @@ def test_student_rows_past_the_range(rows, dtype):
     want = torch.zeros(2, 3000).double().scatter_add(1, ids[:2], -q[:2]) * (dl[:2].double() * tau)[:, None]
     mag = torch.zeros(2, 3000).double().scatter_add(1, ids[:2], 105 * q[:2]) * (dl[:2].double().abs() * tau)[:, None]
     ref.check(grads[:2], (want, mag), 40, "grads")
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.3, 3.0])
+@pytest.mark.parametrize("dtype,size", [("fp32", 1e4), ("fp32", 1e9), ("fp32", 1e30), ("bf16", 1e4), ("bf16", 1e30), ("fp16", 1e4)])
+@pytest.mark.parametrize("rows,vocab", [(7, 300), (5, 20001), (600, 4097)])
+def test_large_logits_at_any_temperature(rows, vocab, dtype, size, tau):
+    """A column above the others by more than exp resolves has p = 1 and they
+    have 0, whatever its quotient by the temperature rounds to: the gradient's
+    rounding of it is the log-sum-exp's.  (The 64-bit value is taken from exact
+    quotients, not from the 32-bit log-sum-exp.)"""
+    z, t, ids, dl = case(rows, vocab, 6, dtype, seed=8)
+    z = (z.double() / 20 * size).to(TYPES[dtype])  # below size
+    best = torch.arange(rows) * 7919 % vocab
+    z[torch.arange(rows), best] = 4 * size
+    z[:, 5] = -size
+    z[0, 5] = -torch.inf
+    ids[1] = -1
+    loss, lse, grads = run(z, t, ids, dl, 3, tau)
+    want, _ = ref.distill_backward(z, t, ids, tau, dl)
+    q, _, some = ref.teacher(t, ids, vocab, tau)
+    p = torch.zeros(rows, vocab).double()
+    p[torch.arange(rows), best] = 1.0
+    by = (dl.double() * tau)[:, None] * some[:, None]
+    at = ids.long().clamp(0, vocab - 1)
+    ref.check(grads, (p.scatter_add(1, at, -q) * by, p.scatter_add(1, at, 105 * q) * by.abs()), 40, "grads")
+    assert (want - p.scatter_add(1, at, -q) * by).abs().max() < 1e-12
+    assert torch.isfinite(lse).all() and not torch.isnan(loss).any()
