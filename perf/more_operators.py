@@ -248,7 +248,7 @@ def _clip(s):
     n = s["scale"] * n
     s["norm_out"].copy_(n)
     factor = (s["scale"] * torch.clamp(s["max_norm"] / (n + _EPS), max=1.0)).float()
-    torch._foreach_copy_(s["flat"], [x.float() * factor for x in s["flat"]])
+    s["flat"] = [x.copy_(x.float() * factor) for x in s["flat"]]
 
 
 def _logits(s):
