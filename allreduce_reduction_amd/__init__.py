@@ -37,7 +37,9 @@ EXPORTS = ("hbmc_comm_create", "hbmc_comm_destroy", "hbmc_allreduce", "hbmc_redu
            "hbmc_comm_set_flow", "hbmc_comm_flow_timeouts", "hbmc_plan_flow", "hbmc_reduce_norm",
            "hbmc_reduce_norm_grad", "hbmc_reduce_norm_grad_workspace", "hbmc_embedding", "hbmc_embedding_grad",
            "hbmc_embedding_grad_workspace", "hbmc_distill_loss", "hbmc_distill_loss_workspace",
-           "hbmc_distill_loss_grad")
+           "hbmc_distill_loss_grad", "hbmc_adjust_logits", "hbmc_quantize_rows", "hbmc_product",
+           "hbmc_gradients_create", "hbmc_gradients_destroy", "hbmc_gradients_workspace", "hbmc_gradients_norm",
+           "hbmc_gradients_clip")
 
 
 class HbmcError(RuntimeError):
@@ -90,6 +92,27 @@ class Distill(ctypes.Structure):
                 ("temperature", ctypes.c_float), ("teacher_logits", ctypes.c_void_p),
                 ("teacher_ids", ctypes.c_void_p)]
 
+
+class Logits(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("vocab", ctypes.c_size_t), ("dtype", ctypes.c_int),
+                ("history", ctypes.c_size_t), ("id_bytes", ctypes.c_int), ("tokens", ctypes.c_void_p),
+                ("length_bytes", ctypes.c_int), ("prompt_lengths", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("biases", ctypes.c_size_t), ("bias_id_bytes", ctypes.c_int), ("bias_ids", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("mask", ctypes.c_void_p)]
+
+
+class Product(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_size_t), ("inner", ctypes.c_size_t), ("channels", ctypes.c_size_t),
+                ("dtype", ctypes.c_int), ("form", ctypes.c_int)]
+
+
+class Gradient(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_size_t), ("dtype", ctypes.c_int), ("copies", ctypes.c_int),
+                ("data", ctypes.POINTER(ctypes.c_void_p))]
+
+
+PRODUCT = {"channels": 0, "partial": 1, "reduce": 2, "scatter": 3}
 
 _lib = None
 
@@ -169,7 +192,15 @@ def load_library():
                 ("hbmc_embedding_grad", [vp, ctypes.POINTER(Embedding), pp, pp, szp, pp, ci, ci, vp, sz, vp]),
                 ("hbmc_distill_loss_workspace", [vp, ctypes.POINTER(Distill), szp]),
                 ("hbmc_distill_loss", [vp, ctypes.POINTER(Distill), pp, fp, fp, vp, sz, vp]),
-                ("hbmc_distill_loss_grad", [vp, ctypes.POINTER(Distill), pp, fp, fp, pp, vp])):
+                ("hbmc_distill_loss_grad", [vp, ctypes.POINTER(Distill), pp, fp, fp, pp, vp]),
+                ("hbmc_adjust_logits", [vp, ctypes.POINTER(Logits), pp, pp, vp]),
+                ("hbmc_quantize_rows", [vp, sz, sz, ci, pp, pp, fp, vp]),
+                ("hbmc_product", [vp, ctypes.POINTER(Product), pp, fp, pp, pp, pp, vp]),
+                ("hbmc_gradients_create", [vp, sz, ctypes.POINTER(Gradient), pp]),
+                ("hbmc_gradients_destroy", [vp]),
+                ("hbmc_gradients_workspace", [vp, szp]),
+                ("hbmc_gradients_norm", [vp, ctypes.c_double, ctypes.c_double, fp, vp, sz, vp]),
+                ("hbmc_gradients_clip", [vp] + [ctypes.c_double] * 4 + [fp, vp, sz, vp])):
             f = getattr(L, name)
             f.restype = ci
             f.argtypes = args
@@ -427,6 +458,55 @@ class Comm:
         self._operate("distill_loss_grad", stream, logits, teacher_logits, teacher_ids, lse, loss_grad, logit_grads,
                       temperature)
 
+    def adjust_logits(self, logits, out=None, *, tokens=None, prompt_lengths=None, lengths=None, repetition=None,
+                      frequency=None, presence=None, bias_ids=None, bias=None, mask=None, stream=None):
+        """Penalties for repeated tokens, biases and a grammar's mask on the
+        next token's logits (see hbmc_adjust_logits), into out (default: in
+        place).
+
+        logits, out: the columns of [rows, vocab] each rank owns.  tokens:
+        [rows, history] (int32 or int64), of which a row's first lengths[row]
+        count (default: all), the first prompt_lengths[row] as its prompt
+        (default: none), the others as its output.  repetition, frequency,
+        presence: fp32 [rows].  bias_ids, bias: [rows, biases] (int32 or int64;
+        fp32).  mask: int32 [rows, ceil(vocab / 32)], bit v % 32 of word v //
+        32 set where column v is allowed.  Tokens and ids outside the
+        vocabulary do not count."""
+        self._operate("adjust_logits", stream, logits, out, tokens, prompt_lengths, lengths, repetition, frequency, presence,
+                      bias_ids, bias, mask)
+
+    def quantize_rows(self, x, q, scale, *, stream=None):
+        """Rows rounded to 8-bit codes with one scale a row (see
+        hbmc_quantize_rows): x, the columns of [rows, width] each rank owns,
+        into q (int8, shaped as x) and scale (fp32 [rows]); x is about q *
+        scale."""
+        self._operate("quantize_rows", stream, x, q, scale)
+
+    def product(self, x, x_scale, w, w_scale, out, *, stream=None):
+        """Each rank's own product of 8-bit codes: out[r] = x_scale * w_scale *
+        (x[r] @ w[r].T) (see hbmc_product).
+
+        With w_scale a list (fp32 [channels of r]), the channels are dealt out:
+        x[r]: int8 [rows, inner] (the same tensor may be given for every rank),
+        w[r]: int8 [channels of r, inner], out[r]: [rows, channels of r].  With
+        w_scale one tensor (fp32 [channels]), the inner width is: x[r]: [rows,
+        inner of r], w[r]: [channels, inner of r], out[r]: [rows, channels],
+        rank r's part of the sum.  x_scale: fp32 [rows]."""
+        form = "channels" if isinstance(w_scale, (list, tuple)) else "partial"
+        self._operate("product", stream, x, x_scale, w, w_scale, out, PRODUCT[form])
+
+    def reduce_product(self, x, x_scale, w, w_scale, out, *, scatter=False, stream=None):
+        """The sum over the ranks of their parts of a product whose inner width
+        is dealt out (see product), on every rank (out[r]: [rows, channels]) or,
+        with scatter, each rank's own rows of it."""
+        self._operate("product", stream, x, x_scale, w, w_scale, out, PRODUCT["scatter" if scatter else "reduce"])
+
+    def gradients(self, *, dealt=None, same=None):
+        """A handle of a training step's gradients (see Gradients): dealt[r]:
+        the tensors that rank r alone holds; same[r]: rank r's copies of the
+        tensors that every rank holds alike."""
+        return Gradients(self, dealt, same)
+
     def set_exec_mode(self, mode: str):
         """Launch form of every call: "auto" (default), "steps", "fused", "columns", "lds", "regs" or
         "flow"."""
@@ -541,6 +621,77 @@ class Comm:
                                 nt.value, ctypes.byref(nt), chunks, nc.value, ctypes.byref(nc)), "hbmc_plan_flow")
         return ([dict(col=t.col, seq=t.seq, step=t.step, chunks=range(t.c_lo, t.c_hi)) for t in tiles[:nt.value]],
                 [dict(begin=c.begin, count=c.count, item=c.item) for c in chunks[:nc.value]])
+
+
+class Gradients:
+    """The gradients of a training step, for their global norm and clipping
+    (see hbmc_gradients_create): made once for buffers that stay from step to
+    step, and kept until close().  Tensors are contiguous, on the current device,
+    fp32, fp16 or bf16 in any mixture, and do not overlap."""
+
+    def __init__(self, comm: Comm, dealt=None, same=None):
+        import torch
+        self._h = ctypes.c_void_p()
+        dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+        def address(t, like):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"gradients are tensors, got {type(t).__name__}")
+            if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"a contiguous tensor on device {dev} is needed, got one on {t.device}")
+            if t.dtype != like.dtype or t.shape != like.shape:
+                raise ValueError("a tensor of `same` has one type and shape on every rank")
+            return t.data_ptr()
+
+        groups = [(t,) for mine in self._ranks(comm, dealt, "dealt") for t in mine]
+        copies = self._ranks(comm, same, "same")
+        if any(len(mine) != len(copies[0]) for mine in copies):
+            raise ValueError("same: every rank holds the same tensors")
+        groups += zip(*copies)
+        table = (Gradient * max(1, len(groups)))()
+        for g, held in zip(table, groups):
+            g.data = (ctypes.c_void_p * len(held))(*[address(t, held[0]) for t in held])
+            g.count, g.dtype, g.copies = held[0].numel(), DTYPE[_torch_dtype_name(held[0])], len(held)
+        _check(load_library().hbmc_gradients_create(comm._h, len(groups), table, ctypes.byref(self._h)),
+               "hbmc_gradients_create")
+        self._keep = groups  # the gradients' memory stays with the handle
+
+    @staticmethod
+    def _ranks(comm, lists, what):
+        lists = [[]] * comm.P if lists is None else [list(mine) for mine in lists]
+        if len(lists) != comm.P:
+            raise ValueError(f"{what}: a list of tensors for each of {comm.P} ranks is needed, got {len(lists)}")
+        return lists
+
+    def _call(self, name, stream, *args):
+        dev = _current_device()
+        rc = getattr(load_operators(), name)(self._h.value or 0, dev, _stream(stream), *args,
+                                             lambda nbytes: _scratch(nbytes, dev, stream))
+        if rc != OK:
+            raise HbmcError(rc, "hbmc_" + name)
+
+    def norm(self, norm, *, norm_type=2.0, scale=1.0, stream=None):
+        """The gradients' global norm times |scale| into norm (fp32, one
+        element): norm_type 1, 2 or infinity."""
+        self._call("gradients_norm", stream, norm, norm_type, scale)
+
+    def clip(self, max_norm, norm, *, norm_type=2.0, scale=1.0, eps=1e-6, stream=None):
+        """Every gradient times scale * min(1, max_norm / (norm + eps)), norm
+        being |scale| times their global norm, which norm (fp32, one element)
+        receives."""
+        self._call("gradients_clip", stream, norm, norm_type, scale, max_norm, eps)
+
+    def close(self) -> None:
+        if self._h:
+            _check(load_library().hbmc_gradients_destroy(self._h), "hbmc_gradients_destroy")
+            self._h = ctypes.c_void_p()
+            self._keep = []
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
 
 
 class Graph:

@@ -388,6 +388,148 @@ hbmc_status_t distill_loss_grad(PyObject* const* a) {
   return hbmc_distill_loss_grad(h.comm, &d, z, lse, dl, g, h.stream);
 }
 
+// A descriptor of hbmc_adjust_logits; nothing is asked of tokens without places.
+hbmc_status_t adjust_logits(PyObject* const* a) {
+  // logits, out, tokens, prompt_lengths, lengths, repetition, frequency, presence, bias_ids, bias, mask
+  const Head h(a);
+  const Call& c = h.call;
+  const Ranks logits(a[4], c, "logits");
+  hbmc_logits_t m = {};
+  int64_t vocab = 0;
+  const int64_t rows = logits.size(0, 0, 2);
+  for (int r = 0; r < c.P; ++r) vocab += logits.size(r, 1, 2);
+  m.rows = static_cast<size_t>(rows);
+  m.vocab = static_cast<size_t>(vocab);
+  m.dtype = static_cast<hbmc_dtype_t>(dtype_code(logits.first(), "logits"));
+  const Split columns{vocab, c.P};
+  void *z[kMaxRanks], *out[kMaxRanks];
+  logits.addresses(logits.dtype(), Always{rows}, columns, false, z);
+  if (a[5] != Py_None) Ranks(a[5], c, "out").addresses(logits.dtype(), Always{rows}, columns, false, out);
+  if (a[6] != Py_None) {
+    const at::Tensor& tokens = tensor(a[6], "tokens");
+    if (tokens.dim() != 2) raise(PyExc_ValueError, "tokens: [rows, history] is needed, got %s", text(tokens.sizes()).c_str());
+    m.id_bytes = id_bytes(tokens, "tokens");
+    m.tokens = c.address(tokens, tokens.scalar_type(), {rows, tokens.size(1)}, "tokens");
+    PyObject* const one = a[7] != Py_None ? a[7] : a[8];
+    const at::ScalarType lengths = one != Py_None ? tensor(one, "lengths").scalar_type() : at::kInt;
+    if (one != Py_None) m.length_bytes = id_bytes(tensor(one, "lengths"), "lengths");
+    const void* const prompts = c.optional(a[7], lengths, {rows}, "prompt_lengths");
+    const void* const all = c.optional(a[8], lengths, {rows}, "lengths");
+    const float* const by[3] = {static_cast<float*>(c.optional(a[9], at::kFloat, {rows}, "repetition")),
+                                static_cast<float*>(c.optional(a[10], at::kFloat, {rows}, "frequency")),
+                                static_cast<float*>(c.optional(a[11], at::kFloat, {rows}, "presence"))};
+    if (tokens.size(1) > 0) {
+      m.history = static_cast<size_t>(tokens.size(1));
+      m.prompt_lengths = prompts;
+      m.lengths = all;
+      m.repetition = by[0];
+      m.frequency = by[1];
+      m.presence = by[2];
+    }
+  } else {
+    for (int i = 7; i <= 11; ++i)
+      if (a[i] != Py_None) raise(PyExc_ValueError, "lengths and penalties go with tokens");
+  }
+  if ((a[12] != Py_None) != (a[13] != Py_None)) raise(PyExc_ValueError, "bias_ids and bias go together");
+  if (a[12] != Py_None) {
+    const at::Tensor& ids = tensor(a[12], "bias_ids");
+    if (ids.dim() != 2) raise(PyExc_ValueError, "bias_ids: [rows, biases] is needed, got %s", text(ids.sizes()).c_str());
+    m.bias_id_bytes = id_bytes(ids, "bias_ids");
+    m.biases = static_cast<size_t>(ids.size(1));
+    m.bias_ids = c.address(ids, ids.scalar_type(), {rows, ids.size(1)}, "bias_ids");
+    m.bias = static_cast<float*>(c.address(a[13], at::kFloat, {rows, ids.size(1)}, "bias"));
+  }
+  m.mask = static_cast<uint32_t*>(c.optional(a[14], at::kInt, {rows, (vocab + 31) / 32}, "mask"));
+  return hbmc_adjust_logits(h.comm, &m, z, a[5] == Py_None ? z : out, h.stream);
+}
+
+hbmc_status_t quantize_rows(PyObject* const* a) {
+  // x, q, scale
+  const Head h(a);
+  const Call& c = h.call;
+  const Ranks x(a[4], c, "x");
+  int64_t width = 0;
+  const int64_t rows = x.size(0, 0, 2);
+  for (int r = 0; r < c.P; ++r) width += x.size(r, 1, 2);
+  const hbmc_dtype_t code = static_cast<hbmc_dtype_t>(dtype_code(x.first(), "x"));
+  const Split columns{width, c.P};
+  void *from[kMaxRanks], *to[kMaxRanks];
+  x.addresses(x.dtype(), Always{rows}, columns, false, from);
+  Ranks(a[5], c, "q").addresses(at::kChar, Always{rows}, columns, false, to);
+  float* scale = static_cast<float*>(c.address(a[6], at::kFloat, {rows}, "scale"));
+  int8_t* q[kMaxRanks];
+  for (int r = 0; r < c.P; ++r) q[r] = static_cast<int8_t*>(to[r]);
+  return hbmc_quantize_rows(h.comm, static_cast<size_t>(rows), static_cast<size_t>(width), code, from, q, scale, h.stream);
+}
+
+hbmc_status_t product(PyObject* const* a) {
+  // x, x_scale, w, w_scale, out, form
+  const Head h(a);
+  const Call& c = h.call;
+  const Ranks x(a[4], c, "x"), w(a[6], c, "w"), out(a[8], c, "out");
+  hbmc_product_t m = {};
+  const int form = static_cast<int>(integer(a[9]));
+  const bool dealt = form == HBMC_PRODUCT_CHANNELS;
+  const int64_t rows = x.size(0, 0, 2);
+  int64_t inner = dealt ? x.size(0, 1, 2) : 0, channels = dealt ? 0 : w.size(0, 0, 2);
+  for (int r = 0; r < c.P; ++r) (dealt ? channels : inner) += dealt ? w.size(r, 0, 2) : x.size(r, 1, 2);
+  m.rows = static_cast<size_t>(rows);
+  m.inner = static_cast<size_t>(inner);
+  m.channels = static_cast<size_t>(channels);
+  m.dtype = static_cast<hbmc_dtype_t>(dtype_code(out.first(), "out"));
+  m.form = static_cast<hbmc_product_form_t>(form);
+  const Split inner_of{inner, c.P}, channels_of{channels, c.P}, rows_of{rows, c.P};
+  const auto in = [&](int r) { return dealt ? inner : inner_of(r); };
+  const auto to = [&](int r) { return dealt ? channels_of(r) : channels; };
+  const auto mine = [&](int r) { return form == HBMC_PRODUCT_SCATTER ? rows_of(r) : rows; };
+  void *px[kMaxRanks], *pw[kMaxRanks], *ps[kMaxRanks], *po[kMaxRanks];
+  x.addresses(at::kChar, Always{rows}, in, false, px);
+  w.addresses(at::kChar, to, in, false, pw);
+  if (dealt) {
+    Ranks(a[7], c, "w_scale").addresses(at::kFloat, to, Always{1}, true, ps);
+  } else {
+    void* const one = c.address(a[7], at::kFloat, {channels}, "w_scale");
+    for (int r = 0; r < c.P; ++r) ps[r] = one;
+  }
+  out.addresses(out.dtype(), mine, to, false, po);
+  const float* x_scale = static_cast<float*>(c.address(a[5], at::kFloat, {rows}, "x_scale"));
+  const int8_t *qx[kMaxRanks], *qw[kMaxRanks];
+  const float* s[kMaxRanks];
+  for (int r = 0; r < c.P; ++r) {
+    qx[r] = static_cast<int8_t*>(px[r]);
+    qw[r] = static_cast<int8_t*>(pw[r]);
+    s[r] = static_cast<float*>(ps[r]);
+  }
+  return hbmc_product(h.comm, &m, qx, x_scale, qw, s, po, h.stream);
+}
+
+double wide_real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+
+// The calls of a gradients' handle: (handle, device, stream, ...).
+hbmc_status_t gradients_call(PyObject* const* a, bool clip, PyObject* alloc) {
+  // norm, norm_type, scale[, max_norm, eps], alloc
+  const hbmc_gradients_t g = static_cast<hbmc_gradients_t>(pointer(a[0]));
+  const Call c{1, static_cast<int>(integer(a[1]))};
+  void* const stream = pointer(a[2]);
+  const at::Tensor& n = tensor(a[3], "norm");
+  if (n.numel() != 1) raise(PyExc_ValueError, "norm: a tensor of one element is needed, got %s", text(n.sizes()).c_str());
+  float* const norm = static_cast<float*>(c.address(n, at::kFloat, n.sizes(), "norm"));
+  const double type = wide_real(a[4]), scale = wide_real(a[5]);
+  const double most = clip ? wide_real(a[6]) : 0.0, eps = clip ? wide_real(a[7]) : 0.0;
+  size_t bytes = 0;
+  const hbmc_status_t st = hbmc_gradients_workspace(g, &bytes);
+  if (st != HBMC_OK) return st;
+  const Scratch ws(alloc, bytes);
+  return clip ? hbmc_gradients_clip(g, type, scale, most, eps, norm, ws.data(), bytes, stream)
+              : hbmc_gradients_norm(g, type, scale, norm, ws.data(), bytes, stream);
+}
+hbmc_status_t gradients_norm(PyObject* const* a) { return gradients_call(a, false, a[6]); }
+hbmc_status_t gradients_clip(PyObject* const* a) { return gradients_call(a, true, a[8]); }
+
 // Entry of one function: its number of arguments, the status it returns, and no
 // C++ exception past it.
 template <hbmc_status_t (*F)(PyObject* const*), Py_ssize_t N>
@@ -417,6 +559,11 @@ PyMethodDef methods[] = {method<reduce_norm, 15>("reduce_norm"),
                          method<embedding_grad, 10>("embedding_grad"),
                          method<distill_loss, 11>("distill_loss"),
                          method<distill_loss_grad, 11>("distill_loss_grad"),
+                         method<adjust_logits, 15>("adjust_logits"),
+                         method<quantize_rows, 7>("quantize_rows"),
+                         method<product, 10>("product"),
+                         method<gradients_norm, 7>("gradients_norm"),
+                         method<gradients_clip, 9>("gradients_clip"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,73 +1,16 @@
 // C entry points of the row operators over the ranks: argument checks and
-// launches (kernels in norm_kernels.hip, embedding_kernels.hip and
-// distill_kernels.hip).
+// launches (kernels in norm_kernels.hip, embedding_kernels.hip,
+// distill_kernels.hip, logit_kernels.hip and product_kernels.hip).
 #include <algorithm>
-#include <vector>
 
 #include "comm.hpp"
 #include "hbmcoll.h"
+#include "rank_args.hpp"
 #include "rowops.hpp"
 
 using namespace hbmc;
 
 namespace {
-
-// Memory ranges of a call.  A range that is written may overlap no other;
-// ranges that are only read may overlap each other.
-class Ranges {
- public:
-  // [p, p + bytes), checked for NULL, alignment and wrap-around; nothing to
-  // check where it holds nothing.
-  void add(const void* p, uint64_t bytes, uint32_t align, bool write) {
-    if (bytes == 0) return;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    if (!a || a % align || a + bytes < a) bad_ = true;
-    all_.push_back({a, a + bytes, write});
-  }
-  void read(const void* p, uint64_t bytes, uint32_t align) { add(p, bytes, align, false); }
-  void write(const void* p, uint64_t bytes, uint32_t align) { add(p, bytes, align, true); }
-  // An output that may be exactly the input `in`, which is then not added.
-  void write_over(const void* p, const void* in, uint64_t bytes, uint32_t align) {
-    write(p, bytes, align);
-    if (in != p) read(in, bytes, align);
-  }
-  bool ok() {
-    if (bad_) return false;
-    std::sort(all_.begin(), all_.end(), [](const Range& x, const Range& y) { return x.lo < y.lo; });
-    uintptr_t any = 0, written = 0;  // ends of the ranges so far, of the written ones
-    for (const Range& r : all_) {
-      if (r.lo < written || (r.write && r.lo < any)) return false;
-      any = std::max(any, r.hi);
-      if (r.write) written = std::max(written, r.hi);
-    }
-    return true;
-  }
-
- private:
-  struct Range {
-    uintptr_t lo, hi;
-    bool write;
-  };
-  std::vector<Range> all_;
-  bool bad_ = false;
-};
-
-// Element size of a type the operators take (0: they do not).
-uint32_t float_bytes(int dtype) { return dtype == HBMC_FP32 || dtype == HBMC_FP16 || dtype == HBMC_BF16 ? elem_bytes(dtype) : 0; }
-
-bool finite(float x) { return x - x == 0.0f; }
-
-constexpr uint64_t kMaxRows = (uint64_t(1) << 31) - 1;
-
-int ranks_of(hbmc_comm_t c) { return c && !c->topos.empty() ? c->topos[0].P : 0; }
-
-// Bytes of a matrix, or false when they do not fit an address.
-bool matrix_bytes(uint64_t rows, uint64_t width, uint32_t e, uint64_t* bytes) {
-  return !__builtin_mul_overflow(rows, width, bytes) && !__builtin_mul_overflow(*bytes, uint64_t(e), bytes) &&
-         *bytes <= uint64_t(PTRDIFF_MAX);
-}
-
-hbmc_status_t hip(hipError_t e) { return e == hipSuccess ? HBMC_OK : HBMC_ERR_HIP; }
 
 // ------------------------------------------------------------------ norms
 
@@ -345,9 +288,164 @@ hbmc_status_t distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* m, const
   return hip(launch_distill_grad(m->dtype, a, static_cast<hipStream_t>(stream)));
 }
 
+// ------------------------------------ penalties, biases and masks on logits
+
+hbmc_status_t adjust_logits(hbmc_comm_t comm, const hbmc_logits_t* m, const void* const logits[], void* const out[], void* stream) {
+  const int P = ranks_of(comm);
+  if (P == 0 || !m) return HBMC_ERR_INVALID_ARG;
+  const uint32_t e = float_bytes(m->dtype);
+  if (e == 0) return m->dtype == HBMC_INT32 || m->dtype == HBMC_INT8 ? HBMC_ERR_UNSUPPORTED : HBMC_ERR_INVALID_ARG;
+  const auto width = [](int b) { return b == 4 || b == 8; };
+  uint64_t bytes;
+  if (m->vocab == 0 || m->vocab > kMaxVocab || m->rows > kMaxRows || !matrix_bytes(m->rows, m->vocab, 4, &bytes) || !logits || !out)
+    return HBMC_ERR_INVALID_ARG;
+  if (m->history > 0 ? !width(m->id_bytes) || ((m->prompt_lengths || m->lengths) && !width(m->length_bytes))
+                     : m->prompt_lengths || m->lengths || m->repetition || m->frequency || m->presence)
+    return HBMC_ERR_INVALID_ARG;
+  if (m->biases > 0 && !width(m->bias_id_bytes)) return HBMC_ERR_INVALID_ARG;
+  if (m->history > kMaxHistory || m->biases > kMaxBias) return HBMC_ERR_UNSUPPORTED;
+  LogitArgs a = {};
+  a.rows = m->rows;
+  a.vocab = static_cast<uint32_t>(m->vocab);
+  a.seg = static_cast<uint32_t>(segment_each(m->vocab, P));
+  a.P = P;
+  a.history = static_cast<uint32_t>(m->history);
+  a.biases = static_cast<uint32_t>(m->biases);
+  a.tile = logit_tile(m->dtype, a.rows, a.seg, P);
+  a.tiles = (a.seg + a.tile - 1) / a.tile;
+  if (a.rows * a.tiles > kMaxLogitTiles / static_cast<uint64_t>(P)) return HBMC_ERR_UNSUPPORTED;
+  a.id_bytes = m->id_bytes;
+  a.length_bytes = m->length_bytes;
+  a.bias_id_bytes = m->bias_id_bytes;
+  a.mask_bytes = (a.vocab + 31) / 32 * 4;
+  Ranges r;
+  if (a.history) {
+    r.read(m->tokens, a.rows * a.history * a.id_bytes, a.id_bytes);
+    a.tokens = static_cast<const unsigned char*>(m->tokens);
+    const auto row = [&](const void* p, uint32_t size) {
+      if (p) r.read(p, a.rows * size, size);
+    };
+    row(a.lengths = static_cast<const unsigned char*>(m->lengths), static_cast<uint32_t>(a.length_bytes));
+    row(a.prompt_lengths = static_cast<const unsigned char*>(m->prompt_lengths), static_cast<uint32_t>(a.length_bytes));
+    row(a.repetition = m->repetition, 4);
+    row(a.frequency = m->frequency, 4);
+    row(a.presence = m->presence, 4);
+  }
+  if (a.biases) {
+    r.read(a.bias_ids = static_cast<const unsigned char*>(m->bias_ids), a.rows * a.biases * a.bias_id_bytes, a.bias_id_bytes);
+    r.read(a.bias = m->bias, a.rows * a.biases * 4, 4);
+  }
+  if (m->mask) r.read(a.mask = reinterpret_cast<const unsigned char*>(m->mask), a.rows * a.mask_bytes, 4);
+  uint32_t over = 0, parts = 0;
+  for (int p = 0; p < P; ++p) {
+    a.logits[p] = static_cast<const unsigned char*>(logits[p]);
+    a.out[p] = static_cast<unsigned char*>(out[p]);
+    const uint64_t mine = a.rows * segment_count(a.vocab, P, p) * e;
+    r.write_over(out[p], logits[p], mine, e);
+    if (mine > 0) ++parts, over += out[p] == logits[p];
+  }
+  if (over != 0 && over != parts) return HBMC_ERR_INVALID_ARG;
+  a.in_place = over != 0;
+  if (!r.ok()) return HBMC_ERR_INVALID_ARG;
+  // without a penalty nothing is asked of the tokens
+  if (!a.repetition && !a.frequency && !a.presence) a.tokens = nullptr;
+  if (a.rows == 0 || (a.in_place && !a.tokens && !a.biases && !a.mask)) return HBMC_OK;
+  return hip(launch_logits(m->dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------- products in 8-bit integers
+
+hbmc_status_t quantize_rows(hbmc_comm_t comm, size_t rows, size_t width, hbmc_dtype_t dtype, const void* const x[],
+                            int8_t* const q[], float* scale, void* stream) {
+  const int P = ranks_of(comm);
+  if (P == 0) return HBMC_ERR_INVALID_ARG;
+  const uint32_t e = float_bytes(dtype);
+  if (e == 0) return dtype == HBMC_INT32 || dtype == HBMC_INT8 ? HBMC_ERR_UNSUPPORTED : HBMC_ERR_INVALID_ARG;
+  uint64_t bytes;
+  if (width == 0 || width > kMaxRows || rows > kMaxRows || !matrix_bytes(rows, width, 4, &bytes) || !x || !q) return HBMC_ERR_INVALID_ARG;
+  QuantizeArgs a = {};
+  a.rows = rows;
+  a.width = static_cast<uint32_t>(width);
+  a.seg = static_cast<uint32_t>(segment_each(width, P));
+  a.P = P;
+  a.scale = scale;
+  Ranges r;
+  r.write(scale, rows * 4, 4);
+  for (int p = 0; p < P; ++p) {
+    const uint64_t mine = rows * segment_count(width, P, p);
+    a.x[p] = static_cast<const unsigned char*>(x[p]);
+    a.q[p] = reinterpret_cast<unsigned char*>(q[p]);
+    r.read(x[p], mine * e, e);
+    r.write(q[p], mine, 1);
+  }
+  if (!r.ok()) return HBMC_ERR_INVALID_ARG;
+  if (rows == 0) return HBMC_OK;
+  return hip(launch_quantize(dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+hbmc_status_t product(hbmc_comm_t comm, const hbmc_product_t* m, const int8_t* const x[], const float* x_scale,
+                      const int8_t* const w[], const float* const w_scale[], void* const out[], void* stream) {
+  const int P = ranks_of(comm);
+  if (P == 0 || !m) return HBMC_ERR_INVALID_ARG;
+  const uint32_t e = float_bytes(m->dtype);
+  if (e == 0) return m->dtype == HBMC_INT32 || m->dtype == HBMC_INT8 ? HBMC_ERR_UNSUPPORTED : HBMC_ERR_INVALID_ARG;
+  const int form = static_cast<int>(m->form);
+  uint64_t bytes;
+  if (form < HBMC_PRODUCT_CHANNELS || form > HBMC_PRODUCT_SCATTER || m->rows > kMaxRows || m->inner == 0 || m->channels == 0 ||
+      m->channels > kMaxRows || !matrix_bytes(m->rows, m->channels, 4, &bytes) || !x || !w || !w_scale || !out)
+    return HBMC_ERR_INVALID_ARG;
+  if (m->inner > kMaxInner) return HBMC_ERR_UNSUPPORTED;
+  const bool dealt = form == HBMC_PRODUCT_CHANNELS;
+  ProductArgs a = {};
+  a.rows = static_cast<uint32_t>(m->rows);
+  a.row_seg = static_cast<uint32_t>(std::max<uint64_t>(1, segment_each(m->rows, P)));
+  a.inner = static_cast<uint32_t>(m->inner);
+  a.inner_seg = static_cast<uint32_t>(segment_each(m->inner, P));
+  a.channels = static_cast<uint32_t>(m->channels);
+  a.channel_seg = static_cast<uint32_t>(segment_each(m->channels, P));
+  a.P = P;
+  a.form = form;
+  a.x_scale = x_scale;
+  Ranges r;
+  r.read(x_scale, m->rows * 4, 4);
+  for (int p = 0; p < P; ++p) {
+    const uint64_t inner = dealt ? m->inner : segment_count(m->inner, P, p);
+    const uint64_t channels = dealt ? segment_count(m->channels, P, p) : m->channels;
+    const uint64_t mine = form == HBMC_PRODUCT_SCATTER ? segment_count(m->rows, P, p) : m->rows;
+    a.x[p] = reinterpret_cast<const unsigned char*>(x[p]);
+    a.w[p] = reinterpret_cast<const unsigned char*>(w[p]);
+    a.w_scale[p] = w_scale[p];
+    a.out[p] = static_cast<unsigned char*>(out[p]);
+    if (channels > 0) r.read(x[p], m->rows * inner, 1);
+    r.read(w[p], channels * inner, 1);
+    // the reduced forms read one copy of the channels' scales
+    if (form <= HBMC_PRODUCT_PARTIAL || p == 0) r.read(w_scale[p], channels * 4, 4);
+    r.write(out[p], mine * channels * e, e);
+  }
+  if (!r.ok()) return HBMC_ERR_INVALID_ARG;
+  if (!product_fits(a)) return HBMC_ERR_UNSUPPORTED;
+  if (m->rows == 0) return HBMC_OK;
+  return hip(launch_product(m->dtype, a, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
+
+hbmc_status_t hbmc_adjust_logits(hbmc_comm_t comm, const hbmc_logits_t* adjust, const void* const logits[], void* const out[],
+                                 void* stream) {
+  return no_throw([&] { return adjust_logits(comm, adjust, logits, out, stream); });
+}
+
+hbmc_status_t hbmc_quantize_rows(hbmc_comm_t comm, size_t rows, size_t width, hbmc_dtype_t dtype, const void* const x[],
+                                 int8_t* const q[], float* scale, void* stream) {
+  return no_throw([&] { return quantize_rows(comm, rows, width, dtype, x, q, scale, stream); });
+}
+
+hbmc_status_t hbmc_product(hbmc_comm_t comm, const hbmc_product_t* prod, const int8_t* const x[], const float* x_scale,
+                           const int8_t* const w[], const float* const w_scale[], void* const out[], void* stream) {
+  return no_throw([&] { return product(comm, prod, x, x_scale, w, w_scale, out, stream); });
+}
 
 hbmc_status_t hbmc_reduce_norm(hbmc_comm_t comm, const hbmc_norm_t* norm, const void* const parts[], const void* const residual[],
                                void* const residual_out[], void* const out[], void* const sums[], void* stream) {

@@ -1,5 +1,6 @@
-// Host <-> kernel interface of the row operators (norms at a block's end,
-// embedding, distillation loss) and the device helpers they share.
+// Host <-> kernel interface of the operators over the ranks (norms at a block's
+// end, embedding, distillation loss, gradient clipping, logits' penalties and
+// masks, 8-bit products) and the device helpers they share.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -138,6 +139,95 @@ uint32_t distill_pieces(int dtype, bool grad, uint64_t seg);
 uint64_t distill_workspace(int dtype, const DistillArgs& a);  // bytes of the loss
 hipError_t launch_distill(int dtype, const DistillArgs& a, hipStream_t stream);
 hipError_t launch_distill_grad(int dtype, const DistillArgs& a, hipStream_t stream);
+
+// ------------------------------------------- norm and clipping of gradients
+
+// A piece of a gradient tensor, a workgroup's work at a time.
+struct GradPiece {
+  unsigned char* data;
+  uint64_t offset;  // bytes into the tensor: the piece's place in the other copies
+  uint32_t count;   // elements
+  uint32_t dtype;
+  uint32_t first;   // of the other copies' addresses
+  uint32_t copies;  // buffers that hold the tensor, `data`'s included
+};
+
+struct GradArgs {
+  const GradPiece* pieces;
+  unsigned char* const* others;  // the tensors' other copies
+  uint32_t n;
+  uint32_t sums;  // partial sums in `partial`
+  int norm;       // 1, 2, or 0 for the largest value
+  bool clip;      // whether the gradients are scaled
+  bool stream;    // stores past the memory-side cache
+  double scale, max_norm, eps;
+  double* partial;
+  float* norm_out;
+};
+
+constexpr uint64_t kGradPieceBytes = uint64_t(16) << 10;
+uint32_t grad_sums(uint64_t pieces);  // partial sums of so many pieces (0: none are kept)
+hipError_t launch_grad(const GradArgs& a, hipStream_t stream);
+
+// ------------------------------------ penalties, biases and masks on logits
+
+constexpr uint64_t kMaxHistory = (uint64_t(1) << 19) - 1;  // a column's count and its flags share 32 bits
+constexpr uint64_t kMaxBias = (uint64_t(1) << 12) - 1;
+
+struct LogitArgs {
+  const unsigned char* logits[kMaxRanks];
+  unsigned char* out[kMaxRanks];
+  uint64_t rows;
+  uint32_t vocab, seg;
+  uint32_t tile, tiles;  // columns of a workgroup, tiles of a rank's columns
+  int P, id_bytes, length_bytes, bias_id_bytes;
+  bool in_place;
+  const unsigned char* tokens;
+  const unsigned char* prompt_lengths;
+  const unsigned char* lengths;
+  uint32_t history;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const unsigned char* bias_ids;
+  const float* bias;
+  uint32_t biases;
+  const unsigned char* mask;
+  uint32_t mask_bytes;  // of a row
+};
+uint32_t logit_tile(int dtype, uint64_t rows, uint64_t seg, int P);
+constexpr uint64_t kMaxLogitTiles = uint64_t(1) << 22;  // of a call: below 2^32 threads
+hipError_t launch_logits(int dtype, const LogitArgs& a, hipStream_t stream);
+
+// ---------------------------------------------- products in 8-bit integers
+
+constexpr uint64_t kMaxInner = (uint64_t(1) << 17) - 1;  // sums of products of 8-bit values stay below 2^31
+
+struct QuantizeArgs {
+  const unsigned char* x[kMaxRanks];
+  unsigned char* q[kMaxRanks];
+  float* scale;
+  uint64_t rows;
+  uint32_t width, seg;
+  int P;
+};
+hipError_t launch_quantize(int dtype, const QuantizeArgs& a, hipStream_t stream);
+
+struct ProductArgs {
+  const unsigned char* x[kMaxRanks];
+  const unsigned char* w[kMaxRanks];
+  const float* w_scale[kMaxRanks];
+  unsigned char* out[kMaxRanks];
+  const float* x_scale;
+  uint32_t rows, row_seg;           // rows, rows that a rank owns
+  uint32_t inner, inner_seg;        // inner width, of one rank
+  uint32_t channels, channel_seg;   // channels, of one rank
+  int P;
+  int form;  // hbmc_product_form_t
+};
+// Whether its launch stays below 2^32 threads.
+bool product_fits(const ProductArgs& a);
+hipError_t launch_product(int dtype, const ProductArgs& a, hipStream_t stream);
 
 // --------------------------------------------------------- device helpers
 

@@ -502,8 +502,10 @@ hbmc_status_t hbmc_graph_destroy(hbmc_graph_t graph);
 /*
  * Operators of a model at the places where its own row work meets a
  * collective over the ranks: the norms at a block's end over the ranks'
- * partial sums, the embedding whose rows are dealt out to the ranks, and the
- * loss over logits whose columns are dealt out to the ranks.  Each does the
+ * partial sums, the embedding whose rows are dealt out to the ranks, the loss
+ * over logits whose columns are dealt out to the ranks and what is done to them
+ * before a token is chosen, products whose channels or inner width are dealt out,
+ * and the norm and clipping of the gradients that a collective leaves.  Each does the
  * collective's additions and copies itself, in one pass over the ranks'
  * buffers; the communicator gives the number of ranks P (its algorithm plays
  * no part: sums over ranks are taken in 32 bits, ranks ascending, and rounded
@@ -645,6 +647,132 @@ hbmc_status_t hbmc_distill_loss(hbmc_comm_t comm, const hbmc_distill_t* distill,
 hbmc_status_t hbmc_distill_loss_grad(hbmc_comm_t comm, const hbmc_distill_t* distill, const void* const logits[],
                                      const float* lse, const float* loss_grad, void* const logit_grads[],
                                      void* stream);
+
+/*
+ * Penalties for repeated tokens, biases and a grammar's mask on the logits of
+ * the next token, rank r holding the columns of [rows][vocab] that it owns as a
+ * contiguous [rows][columns of r].  For column v of a row, in 32 bits:
+ *   - seen anywhere in the row's tokens: z = z > 0 ? z / repetition : z * repetition;
+ *   - c times in its output, c > 0: z = z - frequency * c - presence;
+ *   - named by biases: z = z + their sum (in list order);
+ *   - forbidden by the mask: z = -infinity, whatever it was.
+ * A row's tokens are the first lengths[row] of its `history` places, of which
+ * the first prompt_lengths[row] are its prompt and the others its output (lengths
+ * are taken into [0, history], a prompt's into [0, length]); tokens and bias ids
+ * outside [0, vocab) do not count.  Each result is rounded once; a column that
+ * nothing names keeps its bits.  vocab is at most 2^30.
+ */
+typedef struct {
+  size_t rows, vocab;
+  hbmc_dtype_t dtype;
+  size_t history;             /* places of a row of tokens (below 2^19); 0: no tokens       */
+  int id_bytes;               /* width of the tokens: 4 or 8 (signed)                       */
+  const void* tokens;         /* [rows][history]                                            */
+  int length_bytes;           /* width of the lengths: 4 or 8 (signed)                      */
+  const void* prompt_lengths; /* [rows], or NULL: no prompts                                */
+  const void* lengths;        /* [rows], or NULL: rows are full                             */
+  const float* repetition;    /* [rows] each, or NULL: no such penalty                      */
+  const float* frequency;
+  const float* presence;
+  size_t biases;              /* biases of a row (below 4096); 0: none                      */
+  int bias_id_bytes;          /* 4 or 8 (signed)                                            */
+  const void* bias_ids;       /* [rows][biases]                                             */
+  const float* bias;          /* [rows][biases]                                             */
+  const uint32_t* mask;       /* [rows][ceil(vocab / 32)], or NULL: column v is allowed where
+                                 bit v % 32 of word v / 32 is set                           */
+} hbmc_logits_t;
+
+/* out[r] may be logits[r], then for every rank.  HBMC_ERR_UNSUPPORTED: longer
+ * histories or more biases; more than 2^22 tiles in all (a tile: a rank's columns
+ * of a row, or 4096 of them at least). */
+hbmc_status_t hbmc_adjust_logits(hbmc_comm_t comm, const hbmc_logits_t* adjust, const void* const logits[],
+                                 void* const out[], void* stream);
+
+/*
+ * Rows rounded to 8-bit codes with one scale a row, over all ranks: rank r holds
+ * the columns of [rows][width] that it owns, as a contiguous [rows][columns of
+ * r], and receives their codes.  With m = max |x| over the row, in 32 bits,
+ *   scale = m / 127,  q = x * (1 / m * 127), rounded to nearest even, in [-127, 127].
+ * A row whose 1 / m * 127 is no finite number (zeros, or nothing above 3.7e-37) has
+ * scale 0 and zeros; one that holds a NaN or an infinity has scale NaN and zeros,
+ * so that a product with it is NaN.  Tokens and, row for channel, weights are
+ * rounded by it.
+ */
+hbmc_status_t hbmc_quantize_rows(hbmc_comm_t comm, size_t rows, size_t width, hbmc_dtype_t dtype, const void* const x[],
+                                 int8_t* const q[], float* scale, void* stream);
+
+/*
+ * Products of codes, with a scale for each token and each channel:
+ *   y[t][n] = x_scale[t] * w_scale[n] * sum over k of x[t][k] * w[n][k],
+ * the sum in whole numbers (exact), then scaled in 32 bits (token's scale first)
+ * and rounded once.  The inner width is at most 131071 in all.  Where the inner
+ * width is dealt out, the scales are those of whole rows (hbmc_quantize_rows).
+ */
+typedef enum {
+  /* channels dealt out: x[r] [rows][inner] on each rank (they may be one buffer), w[r]
+   * [channels of r][inner], w_scale[r] [channels of r], out[r] [rows][channels of r] */
+  HBMC_PRODUCT_CHANNELS = 0,
+  /* inner width dealt out: x[r] [rows][inner of r], w[r] [channels][inner of r], w_scale[r]
+   * [channels] (may be one buffer); out[r] [rows][channels], each rank's own part of the sum */
+  HBMC_PRODUCT_PARTIAL = 1,
+  /* inputs as for PARTIAL (w_scale[0] alone is read); out[r] [rows][channels], the sum over the
+   * ranks on every rank */
+  HBMC_PRODUCT_REDUCE = 2,
+  /* inputs as for REDUCE; out[r] the sum's rows that rank r owns */
+  HBMC_PRODUCT_SCATTER = 3
+} hbmc_product_form_t;
+
+typedef struct {
+  size_t rows, inner, channels;
+  hbmc_dtype_t dtype; /* of out */
+  hbmc_product_form_t form;
+} hbmc_product_t;
+
+/* HBMC_ERR_UNSUPPORTED: a wider inner width, or 2^24 tiles of 64 x 64 results and more. */
+hbmc_status_t hbmc_product(hbmc_comm_t comm, const hbmc_product_t* prod, const int8_t* const x[], const float* x_scale,
+                           const int8_t* const w[], const float* const w_scale[], void* const out[], void* stream);
+
+/*
+ * The gradients of a training step: their global norm, and their clipping.  The
+ * handle keeps a table of them on the device, made once (gradients stay where
+ * they are from step to step): hbmc_gradients_create allocates it, copies it and
+ * waits for the copy (not while the calling thread captures a stream), and
+ * hbmc_gradients_destroy frees it (after the device's work).  The calls between
+ * do neither and may be captured.
+ *
+ * A tensor has one buffer (what one rank holds alone: a share that a
+ * reduce-scatter dealt out, a dealt-out weight's gradient), or one on each of the
+ * P ranks that hold the same values (as an AllReduce leaves them): data[0]'s are
+ * read, and every buffer is written from them.  Tensors of several types may be
+ * mixed; buffers of a handle must not overlap.  The handle does not need the
+ * communicator afterwards, works on the device current at its creation (else
+ * HBMC_ERR_INVALID_ARG), and must outlive graphs that hold its calls.
+ */
+typedef struct {
+  size_t count;
+  hbmc_dtype_t dtype; /* HBMC_FP32, HBMC_FP16 or HBMC_BF16 */
+  int copies;         /* 1 or P                            */
+  void* const* data;  /* [copies] device pointers          */
+} hbmc_gradient_t;
+typedef struct hbmc_gradients* hbmc_gradients_t;
+hbmc_status_t hbmc_gradients_create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t tensors[], hbmc_gradients_t* out);
+hbmc_status_t hbmc_gradients_destroy(hbmc_gradients_t g);
+hbmc_status_t hbmc_gradients_workspace(hbmc_gradients_t g, size_t* bytes);
+
+/* norm[0] = |scale| * (sum over all tensors of |g|^norm_type)^(1 / norm_type),
+ * each tensor once, for norm_type 1, 2 or infinity (the largest |g|), in 64 bits
+ * and a fixed order, rounded once.  NaN where a gradient is NaN. */
+hbmc_status_t hbmc_gradients_norm(hbmc_gradients_t g, double norm_type, double scale, float* norm, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* The same, then every gradient g = g * f with f = scale * min(1, max_norm /
+ * (norm + eps)), f rounded to 32 bits and each product once to its type: scale is
+ * a factor that the gradients are still to have (1 / P where a sum over ranks is
+ * to be a mean, the inverse of a loss scale).  Where f is 1 nothing is written.  A
+ * norm of infinity gives f = 0, a NaN gives NaN throughout.  max_norm >= 0
+ * (infinity: scale alone), eps >= 0 and finite. */
+hbmc_status_t hbmc_gradients_clip(hbmc_gradients_t g, double norm_type, double scale, double max_norm, double eps,
+                                  float* norm, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* hbmc_status_string(hbmc_status_t status);
