@@ -12,64 +12,141 @@ namespace hbmc {
 namespace dev {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(1)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint32_t u32_any __attribute__((aligned(1)));
 
 // ------------------------------------------------------- rounding to 8 bits
 
-constexpr uint32_t kQuantThreads = 256;
-
-// A workgroup a row: the largest size, as its bits (a NaN's and an infinity's are
-// above every number's), then the codes.
+// The larger sizes of two words of elements: as whole numbers, whose order is
+// theirs (a NaN's and an infinity's are above every number's).
 template <int DT>
-__global__ __launch_bounds__(kQuantThreads) void quantize_rows(QuantizeArgs a) {
+__device__ __forceinline__ uint32_t larger(uint32_t top, uint32_t w) {
+  if constexpr (DT == kF32) {
+    return max(top, w & 0x7fffffffu);
+  } else {
+    typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, top), __builtin_bit_cast(u16x2, w & 0x7fff7fffu)));
+  }
+}
+
+// x * by, rounded to a whole number in the low bits: 1.5 * 2^23 has steps of one.
+__device__ __forceinline__ uint32_t code(float x, float by) { return f2u(x * by + 12582912.0f); }
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
+}
+
+constexpr uint32_t kQuantVectors = 4;  // of a thread, held between the two steps
+
+// A workgroup a row: the largest size, then the codes.  A row of up to four
+// vectors a thread stays in registers and is read once; a longer one (LONG) is
+// read twice.
+template <int DT, uint32_t THREADS, bool LONG>
+__global__ __launch_bounds__(THREADS) void quantize_rows(QuantizeArgs a) {
+  typedef Pack<DT, 16 / Width<DT>::bytes> V;
   typedef Pack<DT, 1> One;
-  constexpr uint32_t E = One::E;
-  __shared__ uint32_t shared[kQuantThreads / 64];
+  constexpr uint32_t E = V::E, VE = 16 / E;
+  __shared__ uint32_t shared[THREADS / 64];
+  constexpr uint32_t WAVES = THREADS / 64;
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t per_rank = (a.seg + 64 * VE - 1) / (64 * VE), all = per_rank * static_cast<uint32_t>(a.P);
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-  uint32_t top = 0;
-  for (int r = 0; r < a.P; ++r) {
-    const uint64_t lo = uint64_t(r) * a.seg;
-    const uint32_t n = lo < a.width ? min(a.seg, a.width - static_cast<uint32_t>(lo)) : 0;
-    for (uint32_t i = threadIdx.x; i < n; i += kQuantThreads) {
-      float f[1];
-      One::widen(One::load(a.x[r] + (row * n + i) * E), f);
-      top = max(top, f2u(f[0]) & 0x7fffffffu);
-    }
-  }
+    // the place of a piece's vectors: rank, the lane's first column, the rank's columns
+    const auto place = [&](uint32_t p, uint32_t* rank, uint32_t* at, uint32_t* n) {
+      *rank = p / per_rank;
+      *at = ((p - *rank * per_rank) * 64 + lane) * VE;
+      const uint64_t lo = uint64_t(*rank) * a.seg;
+      *n = lo < a.width ? min(a.seg, a.width - static_cast<uint32_t>(lo)) : 0;
+    };
+    u32x4 x[kQuantVectors];
+    const auto load = [&](uint32_t p0) {
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-  if (threadIdx.x % 64 == 0) shared[threadIdx.x / 64] = top;
-  __syncthreads();
-  for (uint32_t w = 0; w < kQuantThreads / 64; ++w) top = max(top, shared[w]);
-  const float most = u2f(top), by = 1.0f / most * 127.0f;
-  const bool counts = top < 0x7f800000u && by < __builtin_inff();
-  if (threadIdx.x == 0) a.scale[row] = counts ? most / 127.0f : top < 0x7f800000u ? 0.0f : __builtin_nanf("");
-  for (int r = 0; r < a.P; ++r) {
-    const uint64_t lo = uint64_t(r) * a.seg;
-    const uint32_t n = lo < a.width ? min(a.seg, a.width - static_cast<uint32_t>(lo)) : 0;
-    for (uint32_t i = threadIdx.x; i < n; i += kQuantThreads) {
-      float f[1];
-      One::widen(One::load(a.x[r] + (row * n + i) * E), f);
-      const float c = fminf(fmaxf(__builtin_rintf(f[0] * by), -127.0f), 127.0f);
-      a.q[r][row * n + i] = static_cast<unsigned char>(counts ? static_cast<int>(c) : 0);
+      for (uint32_t j = 0; j < kQuantVectors; ++j) {
+        const uint32_t p = p0 + j * WAVES;
+        x[j] = u32x4{0, 0, 0, 0};
+        if (p >= all) continue;
+        uint32_t rank, at, n;
+        place(p, &rank, &at, &n);
+        const unsigned char* const from = a.x[rank] + (row * n + at) * E;
+        if (at + VE <= n) {
+          x[j] = V::load(from);
+        } else {
+#pragma unroll
+          for (uint32_t e = 0; e < VE; ++e)
+            if (at + e < n) x[j][e * E / 4] |= One::load(from + e * E) << (e * E % 4 * 8);
+        }
+      }
+    };
+    uint32_t top = 0;
+    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * kQuantVectors) {
+      load(p0);
+#pragma unroll
+      for (uint32_t j = 0; j < kQuantVectors; ++j)
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) top = larger<DT>(top, x[j][e]);
+      if (!LONG) break;
     }
-  }
-  __syncthreads();
+    if constexpr (DT == kBF16) top = max(top << 16, top & 0xffff0000u);
+    if constexpr (DT == kF16) top = max(f2u(widen_f16(top & 0xffffu)), f2u(widen_f16(top >> 16)));
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+    if constexpr (THREADS > 64) {
+      if (threadIdx.x % 64 == 0) shared[threadIdx.x / 64] = top;
+      __syncthreads();
+#pragma unroll
+      for (uint32_t w = 0; w < THREADS / 64; ++w) top = max(top, shared[w]);
+      __syncthreads();
+    }
+    const float most = u2f(top), inverse = 1.0f / most * 127.0f;
+    const bool counts = top < 0x7f800000u && inverse < __builtin_inff();
+    const float by = counts ? inverse : 0.0f;
+    if (threadIdx.x == 0) a.scale[row] = counts ? most / 127.0f : top < 0x7f800000u ? 0.0f : __builtin_nanf("");
+    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * kQuantVectors) {
+      if (LONG) load(p0);
+#pragma unroll
+      for (uint32_t j = 0; j < kQuantVectors; ++j) {
+        const uint32_t p = p0 + j * WAVES;
+        if (p >= all) continue;
+        uint32_t rank, at, n, c[VE];
+        place(p, &rank, &at, &n);
+        float f[VE];
+        V::widen(x[j], f);
+#pragma unroll
+        for (uint32_t e = 0; e < VE; ++e) c[e] = counts ? code(f[e], by) : 0;
+        unsigned char* const to = a.q[rank] + row * n + at;
+        if (at + VE <= n) {
+          if constexpr (VE == 8) *reinterpret_cast<u32x2_any*>(to) = u32x2{bytes4(c[0], c[1], c[2], c[3]), bytes4(c[4], c[5], c[6], c[7])};
+          else *reinterpret_cast<u32_any*>(to) = bytes4(c[0], c[1], c[2], c[3]);
+        } else {
+#pragma unroll
+          for (uint32_t e = 0; e < VE; ++e)
+            if (at + e < n) to[e] = static_cast<unsigned char>(c[e]);
+        }
+      }
+      if (!LONG) break;
+    }
   }
 }
 
 // ----------------------------------------------------------------- products
 
-// 16 codes of a row of `n` from position k, zeros past its end.  gfx950 loads
-// global memory at any address.
-__device__ __forceinline__ i32x4 codes16(const unsigned char* row, uint32_t n, uint32_t k) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= n) {
-    typedef i32x4 any __attribute__((aligned(1)));
-    return *reinterpret_cast<const any*>(row + k);
+// Rows of codes at any alignment and of any width.  gfx950 loads global memory at
+// any address, but no load leaves its row: a chunk of 16 codes that would pass the
+// row's end is the row's last 16 instead, tokens and channels alike, and the
+// tokens' lose (keep_from) those that earlier chunks have had, so that a product
+// counts once.  Without a branch at each load, behind which the next would wait.
+__device__ __forceinline__ i32x4 keep_from(i32x4 v, uint32_t first) {  // zeros before byte `first`; from 16 on, all
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) {
+    const uint32_t lost = min(first > 4 * e ? first - 4 * e : 0, 4u);
+    v[e] &= static_cast<int32_t>(static_cast<uint32_t>(0xffffffffull << (8 * lost)));
   }
+  return v;
+}
+// Where a rank has rows of fewer than 16 codes, all go one by one.
+__device__ __forceinline__ i32x4 short_row(const unsigned char* row, uint32_t n, uint32_t k) {
+  i32x4 v = {0, 0, 0, 0};
 #pragma unroll
   for (uint32_t i = 0; i < 16; ++i)
     if (k + i < n) v[i / 4] |= static_cast<int32_t>(static_cast<uint32_t>(row[k + i]) << (8 * (i % 4)));
@@ -98,102 +175,541 @@ __device__ __forceinline__ void store4(unsigned char* out, uint64_t at, uint32_t
   }
 }
 
-constexpr uint32_t kTile = 64, kStep = 64, kPitch = kStep + 16;  // bytes of a staged row: 16 more, so that rows fall on other banks
-
-// A tile of 64 tokens by 64 channels: four waves of 32 by 32, staged through LDS
-// 64 codes of the inner width at a time, at any alignment.
+// Token t's sums of channels [n, n + 4), those below `channels`, to where the form puts them.
 template <int DT>
-__global__ __launch_bounds__(256) void product_tiles(ProductArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char sx[kTile * kPitch], sw[kTile * kPitch];
-  const bool dealt = a.form == 0;  // channels dealt out
-  const uint32_t tiles_n = ((dealt ? a.channel_seg : a.channels) + kTile - 1) / kTile;
-  const uint32_t tiles_t = (a.rows + kTile - 1) / kTile;
+__device__ __forceinline__ void store_results(const ProductArgs& a, uint32_t own, uint32_t channels, uint32_t t, uint32_t n, i32x4 sum,
+                                              float x_scale) {
+  float f[4];
+#pragma unroll
+  for (uint32_t e = 0; e < 4; ++e) f[e] = static_cast<float>(sum[e]) * x_scale * (n + e < channels ? a.w_scale[own][n + e] : 0.0f);
+  const uint32_t left = channels - n;
+  if (a.form <= 1) {
+    store4<DT>(a.out[own], uint64_t(t) * channels + n, left, f);
+  } else if (a.form == 2) {
+    for (int r = 0; r < a.P; ++r) store4<DT>(a.out[r], uint64_t(t) * channels + n, left, f);
+  } else {
+    store4<DT>(a.out[t / a.row_seg], uint64_t(t % a.row_seg) * channels + n, left, f);
+  }
+}
+
+// ---- tiles at any alignment
+
+// A tile of TT tokens by TN channels of WT by WN waves, whose rows may begin and
+// end anywhere: 128 codes of each at a time through registers into one of two
+// halves of LDS, the next on their way while one is multiplied.
+template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, bool SHORT>
+__global__ __launch_bounds__(64 * WT * WN) void product_tiles(ProductArgs a) {
+  constexpr uint32_t WAVES = WT * WN, ROWS = TT + TN, EACH = ROWS / 8 / WAVES;  // rows of a thread's loads
+  constexpr uint32_t FT = TT / WT / 16, FN = TN / WN / 16;
+  static_assert(TT % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0, "a load's rows are of one operand");
+  __shared__ __attribute__((aligned(16))) unsigned char halves[2][ROWS * 128];
+  const bool dealt = a.form == 0;
+  const uint32_t tiles_n = ((dealt ? a.channel_seg : a.channels) + TN - 1) / TN;
+  const uint32_t tiles_t = (a.rows + TT - 1) / TT;
   uint32_t b = blockIdx.x;
   const uint32_t tt = b % tiles_t;
   b /= tiles_t;
-  const uint32_t tn = b % tiles_n, own = b / tiles_n;  // `own`: the rank whose product this is (forms 0 and 1)
+  const uint32_t tn = b % tiles_n, own = b / tiles_n;
   const uint64_t before = uint64_t(own) * a.channel_seg;
   const uint32_t channels = !dealt ? a.channels : before < a.channels ? min(a.channel_seg, a.channels - static_cast<uint32_t>(before)) : 0;
-  const uint32_t t0 = tt * kTile, n0 = tn * kTile;
+  const uint32_t t0 = tt * TT, n0 = tn * TN;
   if (n0 >= channels) return;
-  const int r0 = a.form <= 1 ? static_cast<int>(own) : 0, r1 = a.form <= 1 ? r0 + 1 : a.P;
-  const uint32_t lane = threadIdx.x % 64, wave = threadIdx.x / 64, wt = wave % 2 * 32, wn = wave / 2 * 32;
-  i32x4 acc[2][2] = {};
-  for (int r = r0; r < r1; ++r) {
-    const uint64_t lo = dealt ? 0 : uint64_t(r) * a.inner_seg;
-    const uint32_t inner = dealt ? a.inner : lo < a.inner ? min(a.inner_seg, a.inner - static_cast<uint32_t>(lo)) : 0;
-    const uint32_t row = threadIdx.x / 4, part = threadIdx.x % 4 * 16;
-    for (uint32_t k = 0; k < inner; k += kStep) {
-      i32x4 vx = {0, 0, 0, 0}, vw = {0, 0, 0, 0};
-      if (t0 + row < a.rows) vx = codes16(a.x[r] + uint64_t(t0 + row) * inner, inner, k + part);
-      if (n0 + row < channels) vw = codes16(a.w[r] + uint64_t(n0 + row) * inner, inner, k + part);
-      __syncthreads();
-      *reinterpret_cast<i32x4*>(sx + row * kPitch + part) = vx;
-      *reinterpret_cast<i32x4*>(sw + row * kPitch + part) = vw;
-      __syncthreads();
-      i32x4 fx[2], fw[2];
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t wt = wave % WT * (TT / WT), wn = wave / WT * (TN / WN);
+  // the next 128 codes to load: rank, its inner width, position in it
+  uint32_t rank = a.form <= 1 ? own : 0, k = 0, inner = 0;
+  const uint32_t end = a.form <= 1 ? own + 1 : static_cast<uint32_t>(a.P);
+  const auto open = [&]() {
+    const uint64_t lo = dealt ? 0 : uint64_t(rank) * a.inner_seg;
+    inner = rank >= end || lo >= a.inner ? 0 : dealt ? a.inner : min(a.inner_seg, a.inner - static_cast<uint32_t>(lo));
+    k = 0;
+  };
+  const uint32_t row = wave * 8 + lane / 8, chunk = lane % 8;
+  struct Codes {
+    i32x4 v[EACH];
+    uint32_t lost;  // of the tokens' 16 at the front (see keep_from)
+    bool any = false, last = false;
+  };
+  const auto load = [&](Codes& c) {
+    c.any = inner > 0;
+    if (!c.any) return;
+    c.last = k + 128 > inner;
+    const uint32_t wanted = k + chunk * 16, at = SHORT ? wanted : min(wanted, inner - 16);
+    c.lost = wanted - at;
 #pragma unroll
-      for (uint32_t i = 0; i < 2; ++i) {
-        fx[i] = *reinterpret_cast<const i32x4*>(sx + (wt + i * 16 + lane % 16) * kPitch + lane / 16 * 16);
-        fw[i] = *reinterpret_cast<const i32x4*>(sw + (wn + i * 16 + lane % 16) * kPitch + lane / 16 * 16);
-      }
-#pragma unroll
-      for (uint32_t i = 0; i < 2; ++i)
-#pragma unroll
-        for (uint32_t j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[i][j], 0, 0, 0);
+    for (uint32_t j = 0; j < EACH; ++j) {
+      const bool is_x = j * 8 * WAVES < TT;
+      const uint32_t r = j * 8 * WAVES + row - (is_x ? 0 : TT);
+      // rows past the last one repeat it: their results are not stored
+      const unsigned char* const from = is_x ? a.x[rank] + uint64_t(t0) * inner : a.w[rank] + uint64_t(n0) * inner;
+      const uint32_t off = (is_x ? min(r, a.rows - 1 - t0) : min(r, channels - 1 - n0)) * inner;
+      if constexpr (SHORT) c.v[j] = short_row(from + off, inner, at);
+      else c.v[j] = *reinterpret_cast<const i32x4_any*>(from + (off + at));
     }
+    k += 128;
+    if (k >= inner) {
+      ++rank;
+      open();
+    }
+  };
+  // a row's chunk c lies at place c ^ (row % 8), so that 8 rows' equal chunks lie on all banks
+  const auto put = [&](unsigned char* to, Codes& c) {
+    if (!SHORT && c.last) {
+#pragma unroll
+      for (uint32_t j = 0; j < TT / 8 / WAVES; ++j) c.v[j] = keep_from(c.v[j], c.lost);
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < EACH; ++j)
+      *reinterpret_cast<i32x4*>(to + (j * 8 * WAVES + row) * 128 + (chunk ^ row % 8) * 16) = c.v[j];
+  };
+  i32x4 acc[FT][FN] = {};
+  const auto multiply = [&](const unsigned char* from) {
+#pragma unroll
+    for (uint32_t s = 0; s < 2; ++s) {
+      i32x4 fx[FT], fw[FN];
+      const uint32_t place = ((s * 4 + lane / 16) ^ (lane % 8)) * 16;
+#pragma unroll
+      for (uint32_t j = 0; j < FN; ++j) fw[j] = *reinterpret_cast<const i32x4*>(from + (TT + wn + j * 16 + lane % 16) * 128 + place);
+#pragma unroll
+      for (uint32_t i = 0; i < FT; ++i) fx[i] = *reinterpret_cast<const i32x4*>(from + (wt + i * 16 + lane % 16) * 128 + place);
+#pragma unroll
+      for (uint32_t i = 0; i < FT; ++i)
+#pragma unroll
+        for (uint32_t j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[i][j], 0, 0, 0);
+    }
+  };
+  // Every wave's codes in LDS, and read.  No __syncthreads(): that would wait for
+  // the codes still on their way to registers.
+  const auto meet = []() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  open();
+  Codes first, second;
+  load(first);
+  load(second);
+  if (first.any) put(halves[0], first);
+  meet();
+  bool more = first.any;  // a rank may hold none of the inner width
+  while (more) {          // halves[0] holds the codes to multiply, `second` the next ones, `first` is free
+    load(first);
+    multiply(halves[0]);
+    if (!second.any) break;
+    put(halves[1], second);
+    meet();
+    load(second);
+    multiply(halves[1]);
+    more = first.any;
+    if (more) put(halves[0], first);
+    meet();
   }
 #pragma unroll
-  for (uint32_t i = 0; i < 2; ++i) {
+  for (uint32_t i = 0; i < FT; ++i) {
     const uint32_t t = t0 + wt + i * 16 + lane % 16;
     if (t >= a.rows) continue;
     const float xs = a.x_scale[t];
 #pragma unroll
-    for (uint32_t j = 0; j < 2; ++j) {
+    for (uint32_t j = 0; j < FN; ++j) {
       const uint32_t n = n0 + wn + j * 16 + lane / 16 * 4;
-      if (n >= channels) continue;
-      float f[4];
-#pragma unroll
-      for (uint32_t e = 0; e < 4; ++e)
-        f[e] = static_cast<float>(acc[i][j][e]) * xs * (n + e < channels ? a.w_scale[own][n + e] : 0.0f);
-      const uint32_t left = channels - n;
-      if (a.form <= 1) store4<DT>(a.out[own], uint64_t(t) * channels + n, left, f);
-      else if (a.form == 2) {
-        for (int r = 0; r < a.P; ++r) store4<DT>(a.out[r], uint64_t(t) * channels + n, left, f);
-      } else {
-        store4<DT>(a.out[t / a.row_seg], uint64_t(t % a.row_seg) * channels + n, left, f);
-      }
+      if (n < channels) store_results<DT>(a, own, channels, t, n, acc[i][j], xs);
     }
   }
 }
 
-}  // namespace dev
+// ---- tiles of aligned rows
 
-hipError_t launch_quantize(int dtype, const QuantizeArgs& a, hipStream_t stream) {
-  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
-  if (dtype == dev::kF32) dev::quantize_rows<dev::kF32><<<grid, dev::kQuantThreads, 0, stream>>>(a);
-  else if (dtype == dev::kF16) dev::quantize_rows<dev::kF16><<<grid, dev::kQuantThreads, 0, stream>>>(a);
-  else dev::quantize_rows<dev::kBF16><<<grid, dev::kQuantThreads, 0, stream>>>(a);
-  return hipGetLastError();
+// A buffer resource of `bytes` from p: loads past its end give zeros.
+__device__ __forceinline__ i32x4 resource(const unsigned char* p, uint32_t bytes) {
+  const uint64_t at = reinterpret_cast<uint64_t>(p);
+  return i32x4{static_cast<int32_t>(at), static_cast<int32_t>(at >> 32 & 0xffff), static_cast<int32_t>(bytes), 0x00020000};
 }
+
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+
+// 16 bytes a lane from `at` of the resource to 1 KiB of LDS.  In assembly, since
+// the compiler's own form makes it wait for every such load before a read of LDS;
+// there is no register that it fills, and the kernel counts the loads itself.  (M0,
+// the place in LDS, is no register that the compiler hands out, and nothing else in
+// these kernels reads it.)
+__device__ __forceinline__ void load_lds(i32x4 from, uint32_t at, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(at), "s"(from), "s"(to));
+}
+
+constexpr uint32_t kWide = 128;  // codes of the inner width in a stage: a row of LDS
+
+template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, uint32_t STAGES, bool TURN>
+__global__ __launch_bounds__(64 * WT * WN) void product_wide(ProductArgs a) {
+  constexpr uint32_t WAVES = WT * WN, ROWS = TT + TN, LOADS = ROWS / 8 / WAVES;  // a wave's loads of a stage, 8 rows each
+  constexpr uint32_t FT = TT / WT / 16, FN = TN / WN / 16;
+  static_assert(TT % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0, "a load's rows are of one operand");
+  static_assert(STAGES >= 2 && (STAGES - 1) * LOADS < 64, "counted in the hardware's six bits");
+  constexpr uint32_t STAGE = ROWS * kWide;
+  __shared__ __attribute__((aligned(1024))) unsigned char stages[STAGES * STAGE];
+  const bool dealt = a.form == 0;
+  const uint32_t tiles_n = ((dealt ? a.channel_seg : a.channels) + TN - 1) / TN;
+  const uint32_t tiles_t = (a.rows + TT - 1) / TT;
+  // workgroups go to the eight XCDs in turn: each takes a run of tiles, four
+  // tiles of tokens deep, that share rows in its L2
+  uint32_t b = blockIdx.x;
+  if (gridDim.x % 8 == 0) b = b % 8 * (gridDim.x / 8) + b / 8;
+  const uint32_t own = b / (tiles_t * tiles_n);
+  b -= own * tiles_t * tiles_n;
+  const uint32_t group = b / (4 * tiles_n), deep = min(4u, tiles_t - 4 * group);
+  b -= group * 4 * tiles_n;
+  const uint32_t tt = 4 * group + b % deep, tn = b / deep;
+  const uint64_t before = uint64_t(own) * a.channel_seg;
+  const uint32_t channels = !dealt ? a.channels : before < a.channels ? min(a.channel_seg, a.channels - static_cast<uint32_t>(before)) : 0;
+  const uint32_t t0 = tt * TT, n0 = tn * TN;
+  if (n0 >= channels) return;
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t wt = wave % WT * (TT / WT), wn = wave / WT * (TN / WN);
+  const uint32_t rows_t = min(TT, a.rows - t0), rows_n = min(TN, channels - n0);
+
+  // the next stage to load: rank, its inner width, position in it
+  uint32_t rank = a.form <= 1 ? own : 0, k = 0, inner = 0, left = 0, todo = 0;
+  const uint32_t end = a.form <= 1 ? own + 1 : static_cast<uint32_t>(a.P);
+  for (uint32_t r = rank; r < end; ++r) {
+    const uint64_t lo = dealt ? 0 : uint64_t(r) * a.inner_seg;
+    if (lo < a.inner) left += ((dealt ? a.inner : min(a.inner_seg, a.inner - static_cast<uint32_t>(lo))) + kWide - 1) / kWide;
+  }
+  // a wave's load: 8 rows of 8 chunks of 16 codes; row r's chunk c lies at place
+  // c ^ (r % 8) of its row, so that 8 rows' equal chunks lie on all banks
+  const uint32_t row = lane / 8, chunk = (lane % 8 ^ row) * 16;
+  const uint32_t turned = TURN ? blockIdx.x : 0;
+  i32x4 px = resource(nullptr, 0), pw = px;
+  uint32_t place = 0;  // the lane's in the first of its loads
+  const auto open = [&]() {
+    const uint64_t lo = dealt ? 0 : uint64_t(rank) * a.inner_seg;
+    inner = rank >= end || lo >= a.inner ? 0 : dealt ? a.inner : min(a.inner_seg, a.inner - static_cast<uint32_t>(lo));
+    todo = (inner + kWide - 1) / kWide;
+    k = todo ? (turned % todo) * kWide : 0;
+    if (inner == 0) return;  // past the last: loads give zeros
+    px = resource(a.x[rank] + uint64_t(t0) * inner, rows_t * inner);
+    pw = resource(a.w[rank] + uint64_t(n0) * inner, rows_n * inner);
+    place = (wave * 8 + row) * inner + chunk;
+  };
+  // The j-th of the wave's loads of a stage, and the step to the next stage.
+  const auto load = [&](unsigned char* to, uint32_t j) {
+    const uint32_t at = place + k + (k + chunk < inner ? 0 : 0x40000000);  // chunks past the inner width: zeros
+    const uint32_t first = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_byte*)to)) + wave * 1024;
+    const bool is_x = j < TT / 8 / WAVES;
+    load_lds(is_x ? px : pw, at + (is_x ? j : j - TT / 8 / WAVES) * (WAVES * 8) * inner, first + j * WAVES * 1024);
+  };
+  const auto advance = [&]() {
+    if (inner == 0) return;
+    k = k + kWide < inner ? k + kWide : 0;
+    if (--todo == 0) {
+      ++rank;
+      open();
+    }
+  };
+  const auto load_all = [&](unsigned char* to) {
+#pragma unroll
+    for (uint32_t j = 0; j < LOADS; ++j) load(to, j);
+    advance();
+  };
+  struct Codes {
+    i32x4 w[FN], x[FT];
+  };
+  // The i-th read of 64 codes of a stage: channels, then tokens.
+  const auto read = [&](const unsigned char* from, uint32_t half, uint32_t i, Codes& c) {
+    const uint32_t place_of = ((half * 4 + lane / 16) ^ (lane % 8)) * 16;
+    if (i < FN) c.w[i] = *reinterpret_cast<const i32x4*>(from + (TT + wn + i * 16 + lane % 16) * kWide + place_of);
+    else c.x[i - FN] = *reinterpret_cast<const i32x4*>(from + (wt + (i - FN) * 16 + lane % 16) * kWide + place_of);
+  };
+  i32x4 acc[FT][FN] = {};
+  // The products of 64 codes.  Between the rows of them go the reads of the next 64
+  // (`half` of `from`) and, with `to`, the loads of a stage, one by one: many at once
+  // would fill the memory pipe, and the products behind them would wait.
+  const auto multiply = [&](const Codes& c, const unsigned char* from, uint32_t half, Codes& next, unsigned char* to) {
+#pragma unroll
+    for (uint32_t i = 0; i < FT; ++i) {
+#pragma unroll
+      for (uint32_t r = i * (FT + FN) / FT; r < (i + 1) * (FT + FN) / FT; ++r) read(from, half, r, next);
+      if (to) {
+#pragma unroll
+        for (uint32_t r = i * LOADS / FT; r < (i + 1) * LOADS / FT; ++r) load(to, r);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(c.w[j], c.x[i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // The next stage's loads done (as many as later stages' may be on their way),
+  // every wave's too, and the stage before it read by all.
+  const auto meet = [&]() {
+    constexpr uint32_t pending = (STAGES - 2) * LOADS;
+    // lgkmcnt 0: its reads are done; no access of LDS moves over this
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(pending) : "memory");
+  };
+  Codes first, second;
+  // One stage, whose first 64 codes are read: its others are read under their
+  // products, the next stage's first under the others', and this stage's place is
+  // loaded again once all have read it.
+  const auto step = [&](unsigned char* now, unsigned char* next) {
+    multiply(first, now, 1, second, nullptr);
+    meet();
+    multiply(second, next, 0, first, now);
+    advance();
+    return --left > 0;
+  };
+  open();
+#pragma unroll
+  for (uint32_t s = 0; s < STAGES; ++s) load_all(stages + s * STAGE);
+  {
+    constexpr uint32_t pending = (STAGES - 1) * LOADS;
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(pending) : "memory");
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < FT + FN; ++i) read(stages, 0, i, first);
+  for (bool more = left > 0; more;) {  // (a rank may hold none of the inner width)
+#pragma unroll
+    for (uint32_t s = 0; s < STAGES; ++s)
+      if (!(more = step(stages + s * STAGE, stages + (s + 1) % STAGES * STAGE))) break;
+  }
+  // nothing on its way to LDS, and every stage read by all
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // Results go through LDS, a part of it for each wave, so that rows of a wave's
+  // channels are stored whole (128 bytes and more of a 256 by 256 tile's).
+  typedef Pack<DT, 16 / Width<DT>::bytes> V;
+  typedef Pack<DT, 1> One;
+  constexpr uint32_t E = V::E, VE = 16 / E, NW = TN / WN, PITCH = NW * E + 16, SHARE = STAGES * STAGE / WAVES;
+  constexpr uint32_t FITS = SHARE / PITCH / 16, BATCH = FITS >= FT ? FT : FITS >= FT / 2 ? FT / 2 : FITS >= FT / 4 ? FT / 4 : 1;
+  static_assert(FITS >= 1 && FT % BATCH == 0, "a batch of 16 rows at least");
+  unsigned char* const mine = stages + wave * SHARE;
+#pragma unroll
+  for (uint32_t i0 = 0; i0 < FT; i0 += BATCH) {
+#pragma unroll
+    for (uint32_t i = i0; i < i0 + BATCH; ++i) {
+      const uint32_t t = t0 + wt + i * 16 + lane % 16;
+      const float xs = a.x_scale[min(t, a.rows - 1)];
+#pragma unroll
+      for (uint32_t j = 0; j < FN; ++j) {
+        const uint32_t n = j * 16 + lane / 16 * 4;
+        float f[4];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i][j][e]) * xs * a.w_scale[own][min(n0 + wn + n + e, channels - 1)];
+        unsigned char* const to = mine + ((i - i0) * 16 + lane % 16) * PITCH + n * E;
+        if constexpr (DT == kF32) *reinterpret_cast<u32x4*>(to) = u32x4{f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3])};
+        else *reinterpret_cast<u32x2*>(to) = u32x2{Pack<DT, 8>::narrow2(f[0], f[1]), Pack<DT, 8>::narrow2(f[2], f[3])};
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr uint32_t CHUNKS_ROW = NW * E / 16;
+#pragma unroll
+    for (uint32_t c0 = 0; c0 < BATCH * 16 * CHUNKS_ROW; c0 += 64) {
+      const uint32_t c = c0 + lane, r = c / CHUNKS_ROW, n = n0 + wn + c % CHUNKS_ROW * VE, t = t0 + wt + i0 * 16 + r;
+      if (c0 + 64 > BATCH * 16 * CHUNKS_ROW && c >= BATCH * 16 * CHUNKS_ROW) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c % CHUNKS_ROW * 16);
+      if (t >= a.rows || n >= channels) continue;
+      const uint32_t left_n = channels - n;
+      const auto put = [&](unsigned char* out, uint32_t row_of) {
+        unsigned char* const to = out + (uint64_t(row_of) * channels + n) * E;
+        if (left_n >= VE) {
+          V::store(to, v);
+        } else {
+#pragma unroll
+          for (uint32_t e = 0; e + 1 < VE; ++e)
+            if (e < left_n) One::store(to + e * E, v[e * E / 4] >> (e * E % 4 * 8));
+        }
+      };
+      if (a.form <= 1) {
+        put(a.out[own], t);
+      } else if (a.form == 2) {
+        for (int r2 = 0; r2 < a.P; ++r2) put(a.out[r2], t);
+      } else {
+        put(a.out[t / a.row_seg], t % a.row_seg);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+// ---- up to 16 tokens and few channels
+
+// The weights are read once and nothing else counts.  A workgroup takes 16 tokens
+// by 16 channels, so that few channels still fill the card; its waves take pieces
+// of the inner width in turn, 256 codes of every row straight from memory in the
+// layout that the matrix instruction reads, the next piece in flight while one is
+// multiplied, and their sums are joined through LDS.  Rows of 16 codes at least,
+// at any alignment (see keep_from).
+constexpr uint32_t kFewWaves = 16, kFewSteps = 4;
+
+template <int DT>
+__global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
+  __shared__ i32x4 part[kFewWaves][64];
+  constexpr uint32_t kPiece = 64 * kFewSteps;
+  const bool dealt = a.form == 0;
+  const uint32_t tiles_n = ((dealt ? a.channel_seg : a.channels) + 15) / 16;
+  const uint32_t tn = blockIdx.x % tiles_n, own = blockIdx.x / tiles_n;
+  const uint64_t before = uint64_t(own) * a.channel_seg;
+  const uint32_t channels = !dealt ? a.channels : before < a.channels ? min(a.channel_seg, a.channels - static_cast<uint32_t>(before)) : 0;
+  const uint32_t n0 = tn * 16;
+  if (n0 >= channels) return;
+  const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const uint32_t each = dealt ? a.inner : a.inner_seg, per_rank = (each + kPiece - 1) / kPiece;
+  const uint32_t r0 = a.form <= 1 ? own : 0;
+  const uint32_t pieces = per_rank * (a.form <= 1 ? 1 : static_cast<uint32_t>(a.P));
+  // tokens and channels past the last one repeat it: their results are not stored
+  const uint32_t row_t = min(lane % 16, a.rows - 1), row_n = min(lane % 16, channels - 1 - n0);
+  const auto inner_of = [&](uint32_t rank) {
+    const uint64_t lo = dealt ? 0 : uint64_t(rank) * a.inner_seg;
+    return dealt ? a.inner : lo < a.inner ? min(a.inner_seg, a.inner - static_cast<uint32_t>(lo)) : 0;
+  };
+  struct Codes {
+    i32x4 w[kFewSteps], x[kFewSteps];
+  };
+  const auto load = [&](uint32_t p, Codes& c) {
+    const uint32_t rank = r0 + p / per_rank, k0 = p % per_rank * kPiece, inner = inner_of(rank);
+    if (k0 >= inner) {  // past a rank with fewer pieces
+#pragma unroll
+      for (uint32_t s = 0; s < kFewSteps; ++s) c.x[s] = i32x4{0, 0, 0, 0};
+      return;
+    }
+    const unsigned char* const w = a.w[rank] + uint64_t(n0) * inner;
+#pragma unroll
+    for (uint32_t s = 0; s < kFewSteps; ++s) {
+      const uint32_t k = min(k0 + s * 64 + lane / 16 * 16, inner - 16);
+      c.w[s] = *reinterpret_cast<const i32x4_any*>(w + (row_n * inner + k));
+      c.x[s] = *reinterpret_cast<const i32x4_any*>(a.x[rank] + (row_t * inner + k));
+    }
+  };
+  i32x4 acc = {0, 0, 0, 0};
+  const auto multiply = [&](uint32_t p, Codes& c) {
+    const uint32_t k0 = p % per_rank * kPiece, inner = inner_of(r0 + p / per_rank);
+    if (k0 < inner && k0 + kPiece > inner) {
+#pragma unroll
+      for (uint32_t s = 0; s < kFewSteps; ++s) {
+        const uint32_t k = k0 + s * 64 + lane / 16 * 16;
+        c.x[s] = keep_from(c.x[s], k - min(k, inner - 16));
+      }
+    }
+#pragma unroll
+    for (uint32_t s = 0; s < kFewSteps; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(c.w[s], c.x[s], acc, 0, 0, 0);
+  };
+  Codes first, second;
+  uint32_t p = wave;
+  if (p < pieces) {
+    load(p, first);
+    for (;;) {
+      if (p + kFewWaves < pieces) load(p + kFewWaves, second);
+      multiply(p, first);
+      p += kFewWaves;
+      if (p >= pieces) break;
+      if (p + kFewWaves < pieces) load(p + kFewWaves, first);
+      multiply(p, second);
+      p += kFewWaves;
+      if (p >= pieces) break;
+    }
+  }
+  part[wave][lane] = acc;
+  __syncthreads();
+  if (wave > 0) return;
+  i32x4 sum = part[0][lane];
+#pragma unroll
+  for (uint32_t w = 1; w < kFewWaves; ++w) sum += part[w][lane];
+  const uint32_t t = lane % 16, n = n0 + lane / 16 * 4;
+  if (t < a.rows && n < channels) store_results<DT>(a, own, channels, t, n, sum, a.x_scale[t]);
+}
+
+}  // namespace dev
 
 namespace {
 
-uint64_t tiles_of(const ProductArgs& a, uint64_t tile) {
-  const uint64_t tiles_n = ((a.form == 0 ? a.channel_seg : a.channels) + tile - 1) / tile;
-  return (a.rows + tile - 1) / tile * tiles_n * (a.form <= 1 ? a.P : 1);
+template <int DT>
+hipError_t launch(const QuantizeArgs& a, hipStream_t stream) {
+  constexpr uint32_t VE = 16 / dev::Width<DT>::bytes;
+  const uint64_t pieces = (a.seg + uint64_t(64) * VE - 1) / (64 * VE) * static_cast<uint64_t>(a.P);
+  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
+  // a wave holds up to four pieces
+  if (pieces <= 4) dev::quantize_rows<DT, 64, false><<<grid, 64, 0, stream>>>(a);
+  else if (pieces <= 16) dev::quantize_rows<DT, 256, false><<<grid, 256, 0, stream>>>(a);
+  else if (pieces <= 64) dev::quantize_rows<DT, 1024, false><<<grid, 1024, 0, stream>>>(a);
+  else dev::quantize_rows<DT, 1024, true><<<grid, 1024, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-bool product_fits(const ProductArgs& a) { return tiles_of(a, dev::kTile) < uint64_t(1) << 24; }
+hipError_t launch_quantize(int dtype, const QuantizeArgs& a, hipStream_t stream) {
+  return dtype == dev::kF32 ? launch<dev::kF32>(a, stream) : dtype == dev::kF16 ? launch<dev::kF16>(a, stream) : launch<dev::kBF16>(a, stream);
+}
+
+namespace {
+
+// Tiles of `tokens` by `channels` results.
+uint64_t tiles_of(const ProductArgs& a, uint64_t tokens, uint64_t channels) {
+  const uint64_t tiles_n = ((a.form == 0 ? a.channel_seg : a.channels) + channels - 1) / channels;
+  return (a.rows + tokens - 1) / tokens * tiles_n * (a.form <= 1 ? a.P : 1);
+}
+uint64_t tiles_of(const ProductArgs& a, uint64_t tile) { return tiles_of(a, tile, tile); }
+
+}  // namespace
+
+bool product_fits(const ProductArgs& a) {
+  return tiles_of(a, 64) <= kMaxProductTiles;
+}
+
+namespace {
+
+// Whether every row of codes begins on 16 bytes and holds whole chunks of 16.
+bool whole_chunks(const ProductArgs& a) {
+  const bool dealt = a.form == 0;
+  if ((dealt ? a.inner : a.inner_seg) % 16 != 0 || a.inner % 16 != 0) return false;
+  for (int r = 0; r < a.P; ++r)
+    if ((reinterpret_cast<uintptr_t>(a.x[r]) | reinterpret_cast<uintptr_t>(a.w[r])) % 16 != 0) return false;
+  return true;
+}
+
+template <int DT>
+void launch_few(const ProductArgs& a, hipStream_t stream) {
+  dev::product_few<DT><<<static_cast<uint32_t>(tiles_of(a, 16)), 64 * dev::kFewWaves, 0, stream>>>(a);
+}
+
+template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, bool SHORT = false>
+void launch_any(const ProductArgs& a, hipStream_t stream) {
+  dev::product_tiles<DT, TT, TN, WT, WN, SHORT><<<static_cast<uint32_t>(tiles_of(a, TT, TN)), 64 * WT * WN, 0, stream>>>(a);
+}
+
+template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, uint32_t STAGES, bool TURN = false>
+void launch_wide(const ProductArgs& a, hipStream_t stream) {
+  dev::product_wide<DT, TT, TN, WT, WN, STAGES, TURN><<<static_cast<uint32_t>(tiles_of(a, TT, TN)), 64 * WT * WN, 0, stream>>>(a);
+}
+
+template <int DT>
+hipError_t launch(const ProductArgs& a, hipStream_t stream) {
+  const uint32_t shortest = a.form == 0 ? a.inner : a.inner % a.inner_seg ? a.inner % a.inner_seg : a.inner_seg;
+  // Kinds of tiles by their time: us for a round of 256 of them over 8192 codes (so
+  // much for the first round).  A large tile does more with what it reads, small ones
+  // fill the card sooner.
+  const auto rounds = [](uint64_t tiles) { return static_cast<double>((tiles + 255) / 256); };
+  if (shortest < 16) {
+    launch_any<DT, 64, 64, 2, 2, true>(a, stream);
+  } else if (a.rows <= 16 && tiles_of(a, 16) <= 1024) {
+    launch_few<DT>(a, stream);
+  } else if (!whole_chunks(a)) {
+    if (10 + 27 * rounds(tiles_of(a, 64)) <= 25 + 62 * rounds(tiles_of(a, 128))) launch_any<DT, 64, 64, 2, 2>(a, stream);
+    else launch_any<DT, 128, 128, 2, 4>(a, stream);
+  } else if (a.rows <= 32) {
+    if (tiles_of(a, 32, 64) >= 512) launch_wide<DT, 32, 64, 1, 4, 4, true>(a, stream);
+    else launch_wide<DT, 32, 32, 2, 2, 8>(a, stream);
+  } else if (a.rows <= 64 && tiles_of(a, 64) <= 128) {
+    launch_wide<DT, 64, 32, 2, 2, 4>(a, stream);
+  } else if (a.rows <= 64 && tiles_of(a, 64, 256) >= 256) {
+    launch_wide<DT, 64, 256, 2, 4, 4, true>(a, stream);
+  } else {
+    const double large = 107 * rounds(tiles_of(a, 256)), middle = 38 * rounds(tiles_of(a, 128)), small = 4 + 13 * rounds(tiles_of(a, 64));
+    if (small <= middle && small <= large) launch_wide<DT, 64, 64, 2, 2, 4>(a, stream);
+    else if (middle <= large) launch_wide<DT, 128, 128, 2, 4, 4>(a, stream);
+    else launch_wide<DT, 256, 256, 2, 4, 2>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
 
 hipError_t launch_product(int dtype, const ProductArgs& a, hipStream_t stream) {
-  const uint64_t grid = tiles_of(a, dev::kTile);
-  if (dtype == dev::kF32) dev::product_tiles<dev::kF32><<<static_cast<uint32_t>(grid), 256, 0, stream>>>(a);
-  else if (dtype == dev::kF16) dev::product_tiles<dev::kF16><<<static_cast<uint32_t>(grid), 256, 0, stream>>>(a);
-  else dev::product_tiles<dev::kBF16><<<static_cast<uint32_t>(grid), 256, 0, stream>>>(a);
-  return hipGetLastError();
+  return dtype == dev::kF32 ? launch<dev::kF32>(a, stream) : dtype == dev::kF16 ? launch<dev::kF16>(a, stream) : launch<dev::kBF16>(a, stream);
 }
 
 }  // namespace hbmc

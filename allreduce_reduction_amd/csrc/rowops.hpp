@@ -225,7 +225,7 @@ struct ProductArgs {
   int P;
   int form;  // hbmc_product_form_t
 };
-// Whether its launch stays below 2^32 threads.
+constexpr uint64_t kMaxProductTiles = uint64_t(1) << 22;  // of 64 x 64 results: every launch stays below 2^32 threads
 bool product_fits(const ProductArgs& a);
 hipError_t launch_product(int dtype, const ProductArgs& a, hipStream_t stream);
 

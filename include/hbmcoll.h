@@ -728,7 +728,7 @@ typedef struct {
   hbmc_product_form_t form;
 } hbmc_product_t;
 
-/* HBMC_ERR_UNSUPPORTED: a wider inner width, or 2^24 tiles of 64 x 64 results and more. */
+/* HBMC_ERR_UNSUPPORTED: a wider inner width, or more than 2^22 tiles of 64 x 64 results. */
 hbmc_status_t hbmc_product(hbmc_comm_t comm, const hbmc_product_t* prod, const int8_t* const x[], const float* x_scale,
                            const int8_t* const w[], const float* const w_scale[], void* const out[], void* stream);
 

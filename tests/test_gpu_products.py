@@ -249,3 +249,53 @@ def test_past_32_bit_offsets():
         c.product([torch.ones(t, 64, dtype=torch.int8, device="cuda")], one(t), [torch.ones(65536, 64, dtype=torch.int8, device="cuda")],
                   [one(65536)], [big])
         assert bool((big == 64).all())
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [5, 200, 1100])
+@pytest.mark.parametrize("inner,channels,P", [(48, 64, 3), (1376, 528, 1), (3 * 208, 300, 3), (16, 1030, 1), (2000, 272, 5)])
+def test_inner_widths_that_end_inside_a_stage(form, rows, inner, channels, P):
+    """Whole chunks of 16 codes, but no whole stages of them; neighbouring memory is not zero."""
+    x, out, call = aligned(rows, inner, channels, P, form, seed=5)
+    with hc.Comm(P, "ring") as c:
+        call(c)
+    if form == "partial":
+        for (lo, hi), o in zip(ref.segments(inner, P), out):
+            ref.check(o, step.product(x.q[:, lo:hi], x.xs, x.w[:, lo:hi], x.ws), 3, form)
+    else:
+        for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
+            ref.check(got, x.want, 3, form)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows,inner,channels,P", [(20, 512, 33000, 1), (64, 256, 66000, 2), (64, 272, 16400, 1), (300, 4096, 4096, 2),
+                                                   (2000, 640, 3000, 5), (1500, 333, 5000, 3), (9, 2000, 20000, 2), (9, 2001, 20000, 2)])
+def test_each_kind_of_tile(form, rows, inner, channels, P):
+    """Sizes between which the tile's shape changes."""
+    Layer(rows, inner, channels, BF).run(form, P)
+    x, out, call = aligned(rows, inner, channels, P, form)
+    with hc.Comm(P, "ring") as c:
+        call(c)
+    if form == "partial":
+        for (lo, hi), o in zip(ref.segments(inner, P), out):
+            ref.check(o, step.product(x.q[:, lo:hi], x.xs, x.w[:, lo:hi], x.ws), 3, form)
+    else:
+        for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
+            ref.check(got, x.want, 3, form)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows", [3, 40, 300])
+@pytest.mark.parametrize("inner,P", [(304, 20), (48, 16), (9, 8), (16, 3), (1, 2)])
+def test_ranks_that_hold_none_of_the_inner_width(form, rows, inner, P):
+    """304 over 20 ranks: 16 each, the last one none."""
+    Layer(rows, inner, 70, BF).run(form, P)
+    x, out, call = aligned(rows, inner, 80, P, form)
+    with hc.Comm(P, "ring") as c:
+        call(c)
+    if form == "partial":
+        for (lo, hi), o in zip(ref.segments(inner, P), out):
+            ref.check(o, step.product(x.q[:, lo:hi], x.xs, x.w[:, lo:hi], x.ws), 3, form)
+    else:
+        for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
+            ref.check(got, x.want, 3, form)
