@@ -37,92 +37,92 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
   return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0c0c0400u), __builtin_amdgcn_perm(b, a, 0x0c0c0400u), 0x05040100u);
 }
 
-constexpr uint32_t kQuantVectors = 4;  // of a thread, held between the two steps
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t top_dpp(uint32_t x) {
+  return max(x, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(x), static_cast<int>(x), CTRL, ROWS, 0xf, false)));
+}
+// The largest of a wave, by steps as wave_max's.
+__device__ __forceinline__ uint32_t wave_top(uint32_t x) {
+  x = top_dpp<0x111, 0xf>(x);
+  x = top_dpp<0x112, 0xf>(x);
+  x = top_dpp<0x114, 0xf>(x);
+  x = top_dpp<0x118, 0xf>(x);
+  x = top_dpp<0x142, 0xa>(x);
+  x = top_dpp<0x143, 0xc>(x);
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), 63));
+}
 
-// A workgroup a row: the largest size, then the codes.  A row of up to four
-// vectors a thread stays in registers and is read once; a longer one (LONG) is
-// read twice.
-template <int DT, uint32_t THREADS, bool LONG>
-__global__ __launch_bounds__(THREADS) void quantize_rows(QuantizeArgs a) {
-  typedef Pack<DT, 16 / Width<DT>::bytes> V;
-  typedef Pack<DT, 1> One;
-  constexpr uint32_t E = V::E, VE = 16 / E;
-  __shared__ uint32_t shared[THREADS / 64];
-  constexpr uint32_t WAVES = THREADS / 64;
+// A workgroup a row: the largest size, then the codes.  A row of up to VECTORS
+// pieces a wave (64 vectors of a rank's columns each) stays in registers and is read
+// once; a longer one (LONG) is read twice.  A rank's last vector ends with its
+// columns and overlaps its neighbour, which changes no maximum and writes the same
+// codes twice; VE is 1 where a rank has less than a vector.  No load waits behind a
+// branch.  inverse_of: 2^32 / a rank's pieces, rounded up: exact for the 128
+// pieces that are not LONG.
+template <int DT, int VE, uint32_t THREADS, uint32_t VECTORS, bool LONG>
+__global__ __launch_bounds__(THREADS) void quantize_rows(QuantizeArgs a, uint32_t inverse_of) {
+  typedef Pack<DT, VE> V;
+  constexpr uint32_t E = V::E, WAVES = THREADS / 64;
+  __shared__ uint32_t shared[WAVES];
   const uint32_t lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
-  const uint32_t per_rank = (a.seg + 64 * VE - 1) / (64 * VE), all = per_rank * static_cast<uint32_t>(a.P);
+  const uint32_t per_rank = (a.seg + 64 * VE - 1) / (64 * VE);
+  const uint32_t ranks = (a.width + a.seg - 1) / a.seg, all = per_rank * ranks;  // of those that own columns
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    // the place of a piece's vectors: rank, the lane's first column, the rank's columns
-    const auto place = [&](uint32_t p, uint32_t* rank, uint32_t* at, uint32_t* n) {
-      *rank = p / per_rank;
-      *at = ((p - *rank * per_rank) * 64 + lane) * VE;
-      const uint64_t lo = uint64_t(*rank) * a.seg;
-      *n = lo < a.width ? min(a.seg, a.width - static_cast<uint32_t>(lo)) : 0;
-    };
-    u32x4 x[kQuantVectors];
+    typename V::raw x[VECTORS];
+    // of the wave's j-th piece (the last one again past the end): rank, and the lane's place in the rank's rows
+    uint32_t rank[VECTORS];
+    uint64_t place[VECTORS];
     const auto load = [&](uint32_t p0) {
 #pragma unroll
-      for (uint32_t j = 0; j < kQuantVectors; ++j) {
-        const uint32_t p = p0 + j * WAVES;
-        x[j] = u32x4{0, 0, 0, 0};
-        if (p >= all) continue;
-        uint32_t rank, at, n;
-        place(p, &rank, &at, &n);
-        const unsigned char* const from = a.x[rank] + (row * n + at) * E;
-        if (at + VE <= n) {
-          x[j] = V::load(from);
-        } else {
-#pragma unroll
-          for (uint32_t e = 0; e < VE; ++e)
-            if (at + e < n) x[j][e * E / 4] |= One::load(from + e * E) << (e * E % 4 * 8);
-        }
+      for (uint32_t j = 0; j < VECTORS; ++j) {
+        const uint32_t p = min(p0 + j * WAVES, all - 1);
+        rank[j] = LONG ? p / per_rank : per_rank == 1 ? p : __umulhi(p, inverse_of);
+        const uint32_t n = min(a.seg, a.width - rank[j] * a.seg);
+        place[j] = row * n + min(((p - rank[j] * per_rank) * 64 + lane) * VE, n - VE);
       }
+#pragma unroll
+      for (uint32_t j = 0; j < VECTORS; ++j) x[j] = LONG ? V::load(a.x[rank[j]] + place[j] * E) : V::stream(a.x[rank[j]] + place[j] * E);
     };
     uint32_t top = 0;
-    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * kQuantVectors) {
+    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * VECTORS) {
       load(p0);
 #pragma unroll
-      for (uint32_t j = 0; j < kQuantVectors; ++j)
+      for (uint32_t j = 0; j < VECTORS; ++j) {
+        if constexpr (VE == 1) {
+          top = larger<DT>(top, x[j]);
+        } else {
 #pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) top = larger<DT>(top, x[j][e]);
+          for (uint32_t e = 0; e < 4; ++e) top = larger<DT>(top, x[j][e]);
+        }
+      }
       if (!LONG) break;
     }
     if constexpr (DT == kBF16) top = max(top << 16, top & 0xffff0000u);
     if constexpr (DT == kF16) top = max(f2u(widen_f16(top & 0xffffu)), f2u(widen_f16(top >> 16)));
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    if constexpr (THREADS > 64) {
-      if (threadIdx.x % 64 == 0) shared[threadIdx.x / 64] = top;
+    top = wave_top(top);
+    if constexpr (WAVES > 1) {
+      if (lane == 0) shared[wave] = top;
       __syncthreads();
 #pragma unroll
-      for (uint32_t w = 0; w < THREADS / 64; ++w) top = max(top, shared[w]);
+      for (uint32_t w = 0; w < WAVES; ++w) top = max(top, shared[w]);
       __syncthreads();
     }
     const float most = u2f(top), inverse = 1.0f / most * 127.0f;
     const bool counts = top < 0x7f800000u && inverse < __builtin_inff();
-    const float by = counts ? inverse : 0.0f;
     if (threadIdx.x == 0) a.scale[row] = counts ? most / 127.0f : top < 0x7f800000u ? 0.0f : __builtin_nanf("");
-    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * kQuantVectors) {
+    for (uint32_t p0 = wave; p0 < all; p0 += WAVES * VECTORS) {
       if (LONG) load(p0);
 #pragma unroll
-      for (uint32_t j = 0; j < kQuantVectors; ++j) {
-        const uint32_t p = p0 + j * WAVES;
-        if (p >= all) continue;
-        uint32_t rank, at, n, c[VE];
-        place(p, &rank, &at, &n);
+      for (uint32_t j = 0; j < VECTORS; ++j) {
         float f[VE];
+        uint32_t c[VE];
         V::widen(x[j], f);
 #pragma unroll
-        for (uint32_t e = 0; e < VE; ++e) c[e] = counts ? code(f[e], by) : 0;
-        unsigned char* const to = a.q[rank] + row * n + at;
-        if (at + VE <= n) {
-          if constexpr (VE == 8) *reinterpret_cast<u32x2_any*>(to) = u32x2{bytes4(c[0], c[1], c[2], c[3]), bytes4(c[4], c[5], c[6], c[7])};
-          else *reinterpret_cast<u32_any*>(to) = bytes4(c[0], c[1], c[2], c[3]);
-        } else {
-#pragma unroll
-          for (uint32_t e = 0; e < VE; ++e)
-            if (at + e < n) to[e] = static_cast<unsigned char>(c[e]);
-        }
+        for (uint32_t e = 0; e < VE; ++e) c[e] = counts ? code(f[e], inverse) : 0;
+        unsigned char* const to = a.q[rank[j]] + place[j];
+        if constexpr (VE == 8) *reinterpret_cast<u32x2_any*>(to) = u32x2{bytes4(c[0], c[1], c[2], c[3]), bytes4(c[4], c[5], c[6], c[7])};
+        else if constexpr (VE == 4) *reinterpret_cast<u32_any*>(to) = bytes4(c[0], c[1], c[2], c[3]);
+        else *to = static_cast<unsigned char>(c[0]);
       }
       if (!LONG) break;
     }
@@ -616,16 +616,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
 
 namespace {
 
+template <int DT, int VE>
+void launch(const QuantizeArgs& a, hipStream_t stream) {
+  const uint64_t per_rank = (a.seg + uint64_t(64) * VE - 1) / (64 * VE), pieces = per_rank * ((a.width + a.seg - 1) / a.seg);
+  const uint32_t by = static_cast<uint32_t>(std::min<uint64_t>(UINT32_MAX, ((uint64_t(1) << 32) + per_rank - 1) / per_rank));
+  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
+  if (pieces <= 4) dev::quantize_rows<DT, VE, 64, 4, false><<<grid, 64, 0, stream>>>(a, by);
+  else if (pieces <= 16) dev::quantize_rows<DT, VE, 256, 4, false><<<grid, 256, 0, stream>>>(a, by);
+  else if (pieces <= 64) dev::quantize_rows<DT, VE, 1024, 4, false><<<grid, 1024, 0, stream>>>(a, by);
+  else if (pieces <= 128) dev::quantize_rows<DT, VE, 1024, 8, false><<<grid, 1024, 0, stream>>>(a, by);
+  else dev::quantize_rows<DT, VE, 1024, 4, true><<<grid, 1024, 0, stream>>>(a, by);
+}
+
 template <int DT>
 hipError_t launch(const QuantizeArgs& a, hipStream_t stream) {
   constexpr uint32_t VE = 16 / dev::Width<DT>::bytes;
-  const uint64_t pieces = (a.seg + uint64_t(64) * VE - 1) / (64 * VE) * static_cast<uint64_t>(a.P);
-  const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
-  // a wave holds up to four pieces
-  if (pieces <= 4) dev::quantize_rows<DT, 64, false><<<grid, 64, 0, stream>>>(a);
-  else if (pieces <= 16) dev::quantize_rows<DT, 256, false><<<grid, 256, 0, stream>>>(a);
-  else if (pieces <= 64) dev::quantize_rows<DT, 1024, false><<<grid, 1024, 0, stream>>>(a);
-  else dev::quantize_rows<DT, 1024, true><<<grid, 1024, 0, stream>>>(a);
+  const uint32_t shortest = a.width % a.seg ? a.width % a.seg : a.seg;
+  if (shortest < VE) launch<DT, 1>(a, stream);
+  else launch<DT, VE>(a, stream);
   return hipGetLastError();
 }
 
