@@ -6,7 +6,8 @@
 // their order changes nothing and a token named often is penalised once), adds up
 // the biases of each named column in list order, then passes over its columns
 // once.  Columns that the mask forbids are not read; in place, columns that stay
-// as they are are neither read nor written.
+// as they are are neither read nor written, and without a mask only the named
+// columns are looked at.
 #include <algorithm>
 
 #include "rowops.hpp"
@@ -15,11 +16,16 @@ namespace hbmc {
 namespace dev {
 
 constexpr uint32_t kLogitThreads = 512;
-constexpr uint32_t kLogitVectors = 2;  // of a thread, in flight at once
+constexpr uint32_t kTokenVectors = 2;  // 16-byte loads of tokens of a thread, in flight at once
 
-// A column's word: its count in the row's output (19 bits), whether the row holds
-// it at all, and the place of its bias plus one (12 bits).
-constexpr uint32_t kCountBits = 19, kSeen = 1u << kCountBits, kCount = kSeen - 1, kBiasShift = kCountBits + 1;
+// A column's word: its count in the row's output (19 bits), whether the row's
+// prompt holds it, and the place of its bias plus one (12 bits; 0: none).
+constexpr uint32_t kCountBits = 19, kPrompt = 1u << kCountBits, kCount = kPrompt - 1, kBiasShift = kCountBits + 1;
+static_assert(kCount == kMaxHistory && (1u << (32 - kBiasShift)) - 1 == kMaxBias, "a word's fields");
+
+// Every wave's accesses of LDS done.  No __syncthreads(): that would wait for the
+// loads that are on their way to registers meanwhile.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ int64_t integer_at(const unsigned char* p, int bytes, uint64_t i) {
   return bytes == 8 ? reinterpret_cast<const int64_t*>(p)[i] : reinterpret_cast<const int32_t*>(p)[i];
@@ -30,8 +36,8 @@ struct Penalty {
 };
 
 __device__ __forceinline__ float adjust(float z, uint32_t word, const Penalty& p, const float* sums) {
-  if (word & (kSeen | kCount)) {
-    if (word & kSeen) z = z > 0.0f ? z / p.repetition : z * p.repetition;
+  if (word & (kPrompt | kCount)) {
+    z = z > 0.0f ? z / p.repetition : z * p.repetition;
     const uint32_t count = word & kCount;
     if (count) z = z - p.frequency * static_cast<float>(count) - p.presence;
   }
@@ -39,27 +45,78 @@ __device__ __forceinline__ float adjust(float z, uint32_t word, const Penalty& p
   return z;
 }
 
-// The mask's bits of the `N` columns from column c of a row.
+// The mask's bits of the `N` columns from column c of a row; `one`: in one byte.
 template <uint32_t N>
-__device__ __forceinline__ uint32_t mask_bits(const unsigned char* row, uint32_t bytes, uint32_t c) {
+__device__ __forceinline__ uint32_t mask_bits(const unsigned char* row, uint32_t bytes, uint32_t c, bool one) {
   const uint32_t at = c >> 3;
   uint32_t b = row[at];
-  if ((c & 7) + N > 8 && at + 1 < bytes) b |= static_cast<uint32_t>(row[at + 1]) << 8;
+  if (!one && at + 1 < bytes) b |= static_cast<uint32_t>(row[at + 1]) << 8;
   return (b >> (c & 7)) & ((1u << N) - 1);
 }
 
+// A row's tokens, by the whole workgroup, several 16-byte loads a thread at once;
+// the last few that fill no load are one thread's each.
+template <int BYTES>
+struct Tokens {
+  static constexpr uint32_t N = 16 / BYTES, ROUND = kLogitThreads * kTokenVectors * N;
+  const unsigned char* row;
+  uint32_t history;
+  u32x4 v[kTokenVectors];
+  __device__ __forceinline__ uint32_t place(uint32_t base, uint32_t j) const { return base + (j * kLogitThreads + threadIdx.x) * N; }
+  __device__ __forceinline__ void load(uint32_t base) {
+    typedef u32x4 ids __attribute__((aligned(4)));
+#pragma unroll
+    for (uint32_t j = 0; j < kTokenVectors; ++j) {
+      v[j] = u32x4{~0u, ~0u, ~0u, ~0u};
+      if (place(base, j) + N <= history) v[j] = *reinterpret_cast<const ids*>(row + uint64_t(place(base, j)) * BYTES);
+    }
+  }
+  // f(position, id - col0) for the tokens below `end` that are columns [col0, col0 + n),
+  // the first round loaded before.
+  template <typename F>
+  __device__ __forceinline__ void each(uint32_t end, uint32_t col0, uint32_t n, F&& f) {
+    for (uint32_t base = 0; base < end; base += ROUND) {
+      if (base > 0) load(base);
+#pragma unroll
+      for (uint32_t j = 0; j < kTokenVectors; ++j) {
+        const uint32_t at = place(base, j);
+#pragma unroll
+        for (uint32_t e = 0; e < N; ++e) {
+          const uint32_t c = v[j][e * BYTES / 4] - col0;
+          if (c < n && at + e < end && (BYTES == 4 || v[j][(e * BYTES / 4 + 1) % 4] == 0)) f(at + e, c);
+        }
+      }
+    }
+    const uint32_t last = history / N * N + threadIdx.x;
+    if (threadIdx.x < N && last < end) {
+      const int64_t id = integer_at(row, BYTES, last);
+      if (id >= col0 && id < static_cast<int64_t>(col0) + n) f(last, static_cast<uint32_t>(id - col0));
+    }
+  }
+};
+
+// The type's -infinity, as often as a word holds it.
 template <int DT>
-__global__ __launch_bounds__(kLogitThreads) void adjust_logits(LogitArgs a) {
+constexpr uint32_t kMinusInfinity = DT == kF32 ? 0xff800000u : DT == kF16 ? 0xfc00fc00u : 0xff80ff80u;
+
+constexpr uint32_t kLogitTile = 8192;  // columns of a workgroup at most
+
+// How a tile's columns are passed over.
+enum { kNamed = 0, kInPlace = 1, kApart = 2, kPast = 3 };  // named ones alone, in place; all, in place, to other memory, past the caches
+
+template <int DT, bool LISTS, int PASS, int BYTES>
+__global__ __launch_bounds__(kLogitThreads, 8) void adjust_logits(LogitArgs a) {
   typedef Pack<DT, 16 / Width<DT>::bytes> V;
   typedef Pack<DT, 1> One;
   constexpr uint32_t E = V::E, VE = 16 / E, kAll = (1u << VE) - 1;
+  constexpr uint32_t VECTORS = E == 4 ? 4 : 2;  // of columns of a thread, in flight at once: a tile of 8192
   extern __shared__ __attribute__((aligned(16))) uint32_t words[];
-  const uint32_t per_row = static_cast<uint32_t>(a.P) * a.tiles;
-  const uint64_t row = blockIdx.x / per_row;
-  const uint32_t at = blockIdx.x % per_row, rank = at / a.tiles;
+  __shared__ uint32_t twice;  // whether a column of the tile has several biases
+  const uint64_t row = blockIdx.x;
+  const uint32_t rank = blockIdx.y;
   const uint64_t col = uint64_t(rank) * a.seg;
   const uint32_t cols = col < a.vocab ? min(a.seg, a.vocab - static_cast<uint32_t>(col)) : 0;
-  const uint32_t first = (at % a.tiles) * a.tile;
+  const uint32_t first = blockIdx.z * a.tile;
   if (first >= cols) return;
   const uint32_t n = min(a.tile, cols - first), col0 = static_cast<uint32_t>(col) + first;
   const unsigned char* const in = a.logits[rank] + (row * cols + first) * E;
@@ -68,122 +125,187 @@ __global__ __launch_bounds__(kLogitThreads) void adjust_logits(LogitArgs a) {
   const uint32_t head = min(n, (16 - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out)) & 15)) % 16 / E);
   const uint32_t vectors = (n - head) / VE, tail = head + vectors * VE;
   const uint32_t pad = (4 - head % 4) % 4;  // a vector's words begin on 16 bytes
-  const bool lists = a.tokens || a.biases;
   uint32_t* const word = words + pad;
   float* const sums = reinterpret_cast<float*>(words + (a.tile + 4));
   int32_t* const names = reinterpret_cast<int32_t*>(sums + a.biases);
   Penalty p = {1.0f, 0.0f, 0.0f};
-  if (lists) {
-    for (uint32_t i = threadIdx.x; i < n; i += kLogitThreads) word[i] = 0;
-    for (uint32_t i = threadIdx.x; i < a.biases; i += kLogitThreads) {
-      const int64_t id = integer_at(a.bias_ids, a.bias_id_bytes, row * a.biases + i);
-      names[i] = id >= col0 && id < static_cast<int64_t>(col0) + n ? static_cast<int32_t>(id - col0) : -1;
-      sums[i] = a.bias[row * a.biases + i];
-    }
-    __syncthreads();
+  const unsigned char* const mask = PASS != kNamed && a.mask ? a.mask + row * a.mask_bytes : nullptr;
+  const bool one_byte = (col0 + head) % VE == 0;  // a vector's bits of the mask
+  uint32_t allowed[VECTORS];
+  u32x4 z[VECTORS];
+  const auto bits_of = [&](uint32_t v0) {
+#pragma unroll
+    for (uint32_t j = 0; j < VECTORS; ++j)
+      allowed[j] = mask ? mask_bits<VE>(mask, a.mask_bytes, col0 + head + min(v0 + j * kLogitThreads, vectors - 1) * VE, one_byte) : kAll;
+  };
+  const auto load = [&](uint32_t v, uint32_t j) {
+    const unsigned char* const from = in + uint64_t(head + v * VE) * E;
+    z[j] = PASS == kPast ? V::stream(from) : V::load(from);
+  };
+  // what is read whatever the lists hold: in place, columns that the mask forbids in part
+  const auto load_early = [&](uint32_t v0) {
+#pragma unroll
+    for (uint32_t j = 0; j < VECTORS; ++j)
+      if (v0 + j * kLogitThreads < vectors && allowed[j] != 0 && (PASS != kInPlace || allowed[j] != kAll)) load(v0 + j * kLogitThreads, j);
+  };
+  if constexpr (LISTS) {
+    // All that is known where to find is asked for before the first barrier.
+    Tokens<BYTES> tokens{a.tokens + row * a.history * BYTES, a.tokens ? a.history : 0, {}};
+    uint32_t end = 0, start = 0;
     if (a.tokens) {
+      tokens.load(0);
       int64_t length = a.lengths ? integer_at(a.lengths, a.length_bytes, row) : a.history;
       length = min(max(length, int64_t(0)), static_cast<int64_t>(a.history));
-      int64_t prompt = a.prompt_lengths ? integer_at(a.prompt_lengths, a.length_bytes, row) : 0;
-      prompt = min(max(prompt, int64_t(0)), length);
-      const uint32_t end = static_cast<uint32_t>(length), start = static_cast<uint32_t>(prompt);
-      const uint64_t base = row * a.history;
-      for (uint32_t i = threadIdx.x; i < end; i += kLogitThreads) {
-        const int64_t id = integer_at(a.tokens, a.id_bytes, base + i);
-        if (id >= col0 && id < static_cast<int64_t>(col0) + n) {
-          uint32_t* const w = word + (id - col0);
-          if (i >= start) atomicAdd(w, 1u);
-          if (a.repetition) atomicOr(w, kSeen);
-        }
-      }
+      const int64_t prompt = a.prompt_lengths ? integer_at(a.prompt_lengths, a.length_bytes, row) : 0;
+      end = static_cast<uint32_t>(length);
+      start = static_cast<uint32_t>(min(max(prompt, int64_t(0)), length));
       if (a.repetition) p.repetition = a.repetition[row];
       if (a.frequency) p.frequency = a.frequency[row];
       if (a.presence) p.presence = a.presence[row];
     }
-    // a named column's first entry adds up all of them
-    float total[kMaxBias / kLogitThreads + 1];
-#pragma unroll
-    for (uint32_t h = 0; h < kMaxBias / kLogitThreads + 1; ++h) {
-      const uint32_t i = threadIdx.x + h * kLogitThreads;
-      total[h] = 0.0f;
-      if (i < a.biases && names[i] >= 0) {
-        bool leads = true;
-        for (uint32_t k = 0; k < i; ++k) leads = leads && names[k] != names[i];
-        total[h] = sums[i];
-        for (uint32_t k = i + 1; k < a.biases; ++k)
-          if (names[k] == names[i]) total[h] += sums[k];
-        if (leads) atomicOr(word + names[i], (i + 1) << kBiasShift);
-      }
+    int64_t bias_id = -1;
+    float bias = 0.0f;
+    const auto load_bias = [&](uint32_t i) {
+      bias_id = integer_at(a.bias_ids, a.bias_id_bytes, row * a.biases + i);
+      bias = a.bias[row * a.biases + i];
+    };
+    if (threadIdx.x < a.biases) load_bias(threadIdx.x);
+    if constexpr (PASS != kNamed) {
+      if (vectors > 0) bits_of(threadIdx.x);
     }
+    for (uint32_t i = threadIdx.x; i < (pad + n + 3) / 4; i += kLogitThreads) reinterpret_cast<u32x4*>(words)[i] = u32x4{0, 0, 0, 0};
+    if (threadIdx.x == 0) twice = 0;
+    meet();
+    // Biases add their place plus one to a column's word: of several that name one
+    // column, at most one then finds its own there.
+    for (uint32_t i = threadIdx.x; i < a.biases; i += kLogitThreads) {
+      if (i >= kLogitThreads) load_bias(i);
+      sums[i] = bias;
+      const bool mine = bias_id >= col0 && bias_id < static_cast<int64_t>(col0) + n;
+      names[i] = mine ? static_cast<int32_t>(bias_id - col0) : -1;
+      if (mine) atomicAdd(word + names[i], (i + 1) << kBiasShift);
+    }
+    if constexpr (PASS != kNamed) load_early(threadIdx.x);
+    const bool prompts = a.repetition != nullptr;
+    tokens.each(end, col0, n, [&](uint32_t i, uint32_t c) {
+      if (i >= start) atomicAdd(word + c, 1u);
+      else if (prompts) atomicOr(word + c, kPrompt);
+    });
+    meet();
     if (a.biases) {
-      __syncthreads();
-#pragma unroll
-      for (uint32_t h = 0; h < kMaxBias / kLogitThreads + 1; ++h) {
-        const uint32_t i = threadIdx.x + h * kLogitThreads;
-        if (i < a.biases) sums[i] = total[h];
-      }
-    }
-    __syncthreads();
-  }
-  const unsigned char* const mask = a.mask ? a.mask + row * a.mask_bytes : nullptr;
-  const float masked = -__builtin_inff();
-  for (uint32_t v0 = threadIdx.x; v0 < vectors; v0 += kLogitThreads * kLogitVectors) {
-    u32x4 z[kLogitVectors];
-    uint32_t allowed[kLogitVectors], w[kLogitVectors][VE];
-    bool on[kLogitVectors];
-#pragma unroll
-    for (uint32_t j = 0; j < kLogitVectors; ++j) {
-      const uint32_t v = v0 + j * kLogitThreads, c = head + v * VE;
-      on[j] = v < vectors;
-      allowed[j] = kAll;
-      uint32_t any = 0;
-#pragma unroll
-      for (uint32_t e = 0; e < VE; ++e) w[j][e] = 0;
-      if (on[j]) {
-        if (mask) allowed[j] = mask_bits<VE>(mask, a.mask_bytes, col0 + c);
-        if (lists) {
-#pragma unroll
-          for (uint32_t e = 0; e < VE; e += 4) {
-            const u32x4 four = *reinterpret_cast<const u32x4*>(word + c + e);
-            w[j][e] = four.x, w[j][e + 1] = four.y, w[j][e + 2] = four.z, w[j][e + 3] = four.w;
-            any |= four.x | four.y | four.z | four.w;
-          }
+      for (uint32_t i = threadIdx.x; i < a.biases; i += kLogitThreads)
+        if (names[i] >= 0 && word[names[i]] >> kBiasShift != i + 1) twice = 1;
+      meet();
+      if (twice) {
+        // the first of a column's biases adds up the others in their order; nobody
+        // else reads its sum or writes its word
+        for (uint32_t i = threadIdx.x; i < a.biases; i += kLogitThreads) {
+          if (names[i] < 0) continue;
+          bool leads = true;
+          for (uint32_t k = 0; k < i; ++k) leads = leads && names[k] != names[i];
+          if (!leads) continue;
+          float total = sums[i];
+          for (uint32_t k = i + 1; k < a.biases; ++k)
+            if (names[k] == names[i]) total += sums[k];
+          sums[i] = total;
+          uint32_t* const w = word + names[i];
+          *w = (*w & (kPrompt | kCount)) | (i + 1) << kBiasShift;
         }
-        if (a.in_place && allowed[j] == kAll && any == 0) on[j] = false;
-        else if (allowed[j] != 0) z[j] = V::load(in + uint64_t(c) * E);
+        meet();
+      }
+    }
+    if constexpr (PASS == kNamed) {
+      // each named column by the first thread to come for it
+      const auto visit = [&](uint32_t c) {
+        const uint32_t w = word[c] ? atomicExch(word + c, 0u) : 0;
+        if (w == 0) return;
+        float f[1];
+        One::widen(One::load(in + uint64_t(c) * E), f);
+        f[0] = adjust(f[0], w, p, sums);
+        One::store(out + uint64_t(c) * E, One::narrow(f));
+      };
+      for (uint32_t i = threadIdx.x; i < a.biases; i += kLogitThreads)
+        if (names[i] >= 0) visit(static_cast<uint32_t>(names[i]));
+      if (end > Tokens<BYTES>::ROUND) tokens.load(0);
+      tokens.each(end, col0, n, [&](uint32_t, uint32_t c) { visit(c); });
+      return;
+    }
+  }
+  for (uint32_t v0 = threadIdx.x; v0 < vectors; v0 += kLogitThreads * VECTORS) {
+    if (!LISTS || v0 >= kLogitThreads * VECTORS) {
+      bits_of(v0);
+      load_early(v0);
+    }
+    // the words of vector v of the tile, and whether any of them is not zero
+    const auto words_of = [&](uint32_t v, uint32_t (&w)[VE]) {
+      uint32_t any = 0;
+#pragma unroll
+      for (uint32_t e = 0; e < VE; e += 4) {
+        const u32x4 four = *reinterpret_cast<const u32x4*>(word + head + v * VE + e);
+        w[e] = four.x, w[e + 1] = four.y, w[e + 2] = four.z, w[e + 3] = four.w;
+        any |= four.x | four.y | four.z | four.w;
+      }
+      return any != 0;
+    };
+    bool on[VECTORS], lists[VECTORS];
+#pragma unroll
+    for (uint32_t j = 0; j < VECTORS; ++j) {
+      const uint32_t v = v0 + j * kLogitThreads;
+      uint32_t w[VE];
+      on[j] = v < vectors;
+      lists[j] = LISTS && on[j] && allowed[j] != 0 && words_of(v, w);
+      if constexpr (PASS == kInPlace) {
+        if (on[j] && allowed[j] == kAll) {
+          on[j] = lists[j];
+          if (on[j]) load(v, j);
+        }
       }
     }
 #pragma unroll
-    for (uint32_t j = 0; j < kLogitVectors; ++j) {
+    for (uint32_t j = 0; j < VECTORS; ++j) {
       if (!on[j]) continue;
-      float f[VE];
-      uint32_t any = 0;
-#pragma unroll
-      for (uint32_t e = 0; e < VE; ++e) any |= w[j][e];
-      if (any != 0 || allowed[j] != kAll) {
+      const uint32_t v = v0 + j * kLogitThreads;
+      if (lists[j]) {
+        float f[VE];
+        uint32_t w[VE];
+        words_of(v, w);
         V::widen(z[j], f);
 #pragma unroll
-        for (uint32_t e = 0; e < VE; ++e) {
-          if (w[j][e]) f[e] = adjust(f[e], w[j][e], p, sums);
-          if (!(allowed[j] >> e & 1)) f[e] = masked;
-        }
+        for (uint32_t e = 0; e < VE; ++e)
+          if (w[e]) f[e] = adjust(f[e], w[e], p, sums);
         z[j] = V::narrow(f);
       }
-      V::store(out + uint64_t(head + (v0 + j * kLogitThreads) * VE) * E, z[j]);
+      if (mask) {
+        // -infinity over the forbidden columns' bits
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) {
+          if constexpr (E == 4) {
+            z[j][e] = allowed[j] >> e & 1 ? z[j][e] : kMinusInfinity<DT>;
+          } else {
+            const uint32_t low = static_cast<uint32_t>(static_cast<int32_t>(allowed[j] << (31 - 2 * e)) >> 31) & 0xffffu;
+            const uint32_t high = static_cast<uint32_t>(static_cast<int32_t>(allowed[j] << (30 - 2 * e)) >> 31) & 0xffff0000u;
+            const uint32_t keep = low | high;
+            z[j][e] = (z[j][e] & keep) | (kMinusInfinity<DT> & ~keep);
+          }
+        }
+      }
+      unsigned char* const to = out + uint64_t(head + v * VE) * E;
+      if constexpr (PASS == kPast) V::store_nt(to, z[j]);
+      else V::store(to, z[j]);
     }
   }
   // the single columns: `head` before the vectors and fewer than a vector after
   uint32_t c = threadIdx.x;
   if (c >= head) c += tail - head;
   if (c < n) {
-    const uint32_t w = lists ? word[c] : 0;
-    const bool allowed = !mask || mask_bits<1>(mask, a.mask_bytes, col0 + c);
-    if (!(a.in_place && allowed && w == 0)) {
-      float f[1] = {masked};
-      typename One::raw r = One::narrow(f);
+    const uint32_t w = LISTS ? word[c] : 0;
+    const bool allowed = !mask || mask_bits<1>(mask, a.mask_bytes, col0 + c, true);
+    if (!(PASS == kInPlace && allowed && w == 0)) {
+      typename One::raw r = kMinusInfinity<DT> >> (32 - 8 * E);
       if (allowed) {
         r = One::load(in + uint64_t(c) * E);
         if (w) {
+          float f[1];
           One::widen(r, f);
           f[0] = adjust(f[0], w, p, sums);
           r = One::narrow(f);
@@ -196,18 +318,46 @@ __global__ __launch_bounds__(kLogitThreads) void adjust_logits(LogitArgs a) {
 
 }  // namespace dev
 
-uint32_t logit_tile(int dtype, uint64_t rows, uint64_t seg, int P) {
-  (void)dtype, (void)rows, (void)P;
-  return static_cast<uint32_t>(std::min<uint64_t>(8192, (seg + 3) / 4 * 4));
+// Tiles of 8192 columns, whose words leave a compute unit four workgroups; smaller
+// ones only where they would leave compute units without work, since every tile
+// reads all of its row's tokens.  bf16, 8 ranks of 131072 columns in all, 2048
+// tokens, tiles of 8192, 4096 and 2048: 256 rows 31, 42 and 71 us, 8 rows 6.4, 5.3 and
+// 5.6, one row 5.4, 4.6 and 4.4.
+uint32_t logit_tile(uint64_t rows, uint64_t seg, int P) {
+  uint64_t tile = dev::kLogitTile;
+  while (tile > 2048 && rows * static_cast<uint64_t>(P) * ((seg + tile - 1) / tile) < 512) tile /= 2;
+  return static_cast<uint32_t>(std::min<uint64_t>(tile, (seg + 3) / 4 * 4));
 }
 
-hipError_t launch_logits(int dtype, const LogitArgs& a, hipStream_t stream) {
-  const uint32_t grid = static_cast<uint32_t>(a.rows * a.tiles * static_cast<uint64_t>(a.P));
+namespace {
+
+template <int DT>
+hipError_t launch(const LogitArgs& a, hipStream_t stream) {
+  // rows first: with rows in eights, a row's tiles share an XCD and its tokens the L2
+  const dim3 grid(static_cast<uint32_t>(a.rows), static_cast<uint32_t>(a.P), a.tiles);
   const uint32_t lds = a.tokens || a.biases ? (a.tile + 4 + 2 * a.biases) * 4 : 0;
-  if (dtype == dev::kF32) dev::adjust_logits<dev::kF32><<<grid, dev::kLogitThreads, lds, stream>>>(a);
-  else if (dtype == dev::kF16) dev::adjust_logits<dev::kF16><<<grid, dev::kLogitThreads, lds, stream>>>(a);
-  else dev::adjust_logits<dev::kBF16><<<grid, dev::kLogitThreads, lds, stream>>>(a);
+  const bool lists = a.tokens || a.biases, past = a.rows * a.vocab * dev::Width<DT>::bytes >= kStreamBytes;
+  const int pass = a.in_place ? (a.mask ? dev::kInPlace : dev::kNamed) : past ? dev::kPast : dev::kApart;
+  const auto go = [&](auto kernel) { kernel<<<grid, dev::kLogitThreads, lds, stream>>>(a); };
+  const auto listed = [&](auto bytes) {
+    constexpr int BYTES = decltype(bytes)::value;
+    if (pass == dev::kNamed) go(dev::adjust_logits<DT, true, dev::kNamed, BYTES>);
+    else if (pass == dev::kInPlace) go(dev::adjust_logits<DT, true, dev::kInPlace, BYTES>);
+    else if (pass == dev::kApart) go(dev::adjust_logits<DT, true, dev::kApart, BYTES>);
+    else go(dev::adjust_logits<DT, true, dev::kPast, BYTES>);
+  };
+  if (lists && a.tokens && a.id_bytes == 8) listed(std::integral_constant<int, 8>{});
+  else if (lists) listed(std::integral_constant<int, 4>{});
+  else if (pass == dev::kInPlace) go(dev::adjust_logits<DT, false, dev::kInPlace, 4>);
+  else if (pass == dev::kApart) go(dev::adjust_logits<DT, false, dev::kApart, 4>);
+  else go(dev::adjust_logits<DT, false, dev::kPast, 4>);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_logits(int dtype, const LogitArgs& a, hipStream_t stream) {
+  return dtype == dev::kF32 ? launch<dev::kF32>(a, stream) : dtype == dev::kF16 ? launch<dev::kF16>(a, stream) : launch<dev::kBF16>(a, stream);
 }
 
 }  // namespace hbmc

@@ -311,9 +311,9 @@ hbmc_status_t adjust_logits(hbmc_comm_t comm, const hbmc_logits_t* m, const void
   a.P = P;
   a.history = static_cast<uint32_t>(m->history);
   a.biases = static_cast<uint32_t>(m->biases);
-  a.tile = logit_tile(m->dtype, a.rows, a.seg, P);
+  a.tile = logit_tile(a.rows, a.seg, P);
   a.tiles = (a.seg + a.tile - 1) / a.tile;
-  if (a.rows * a.tiles > kMaxLogitTiles / static_cast<uint64_t>(P)) return HBMC_ERR_UNSUPPORTED;
+  if (a.rows * a.tiles > kMaxLogitTiles / static_cast<uint64_t>(P) || a.tiles > 0xffff) return HBMC_ERR_UNSUPPORTED;
   a.id_bytes = m->id_bytes;
   a.length_bytes = m->length_bytes;
   a.bias_id_bytes = m->bias_id_bytes;

@@ -195,7 +195,7 @@ struct LogitArgs {
   const unsigned char* mask;
   uint32_t mask_bytes;  // of a row
 };
-uint32_t logit_tile(int dtype, uint64_t rows, uint64_t seg, int P);
+uint32_t logit_tile(uint64_t rows, uint64_t seg, int P);
 constexpr uint64_t kMaxLogitTiles = uint64_t(1) << 22;  // of a call: below 2^32 threads
 hipError_t launch_logits(int dtype, const LogitArgs& a, hipStream_t stream);
 

@@ -683,8 +683,8 @@ typedef struct {
 } hbmc_logits_t;
 
 /* out[r] may be logits[r], then for every rank.  HBMC_ERR_UNSUPPORTED: longer
- * histories or more biases; more than 2^22 tiles in all (a tile: a rank's columns
- * of a row, or 4096 of them at least). */
+ * histories or more biases; more than 2^22 tiles in all, or 2^16 - 1 of a rank's
+ * row (a tile: a rank's columns of a row, or 2048 of them at least). */
 hbmc_status_t hbmc_adjust_logits(hbmc_comm_t comm, const hbmc_logits_t* adjust, const void* const logits[],
                                  void* const out[], void* stream);
 

@@ -213,3 +213,32 @@ def test_past_32_bit_offsets():
         c.adjust_logits([z], tokens=tokens, frequency=torch.ones(rows, device="cuda"), mask=mask)
     assert bool((z[:, vocab - 1] == -2).all()) and bool((z[rows - 1, 7 * 32:8 * 32] == -torch.inf).all())
     assert int((z != 0).sum()) == rows + 32
+
+
+@pytest.mark.parametrize("ids", [torch.int32, torch.int64])
+@pytest.mark.parametrize("history", [1, 2, 3, 4, 5, 2047, 2048, 2049, 4095, 4097, 8193])
+@pytest.mark.parametrize("masked", [False, True])
+def test_histories_that_end_inside_a_load(history, ids, masked):
+    for in_place in (False, True):
+        Rows(3, 9001, BF, history, 2, masked, ids=ids).run(1, in_place)
+
+
+@pytest.mark.parametrize("rows,vocab,P", [(1, 16385, 1), (40, 16385, 2), (700, 8193, 1), (130, 20000, 2), (520, 16384, 1)])
+def test_each_length_of_tile(rows, vocab, P):
+    """Tiles of 2048, 4096 and 8192 columns, the last of a rank a few columns short or long."""
+    for in_place in (False, True):
+        Rows(rows, vocab, F16, 30, 3, True).run(P, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_every_bias_names_one_column(in_place):
+    x = Rows(2, 500, F32, 9, 700)
+    x.kw["bias_ids"][:] = 77
+    x.kw["bias_ids"][1, ::2] = 76
+    x.run(3, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("masked", [False, True])
+def test_most_biases_over_the_longest_tile(in_place, masked):
+    Rows(190, 20000, BF, 12, 4095, masked).run(1, in_place)
