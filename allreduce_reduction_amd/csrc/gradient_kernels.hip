@@ -13,8 +13,8 @@
 namespace hbmc {
 namespace dev {
 
-constexpr uint32_t kGradThreads = 256, kGradVectors = 4;  // a piece: four vectors a thread
-static_assert(kGradThreads * kGradVectors * 16 == kGradPieceBytes, "a piece is one round of its workgroup");
+constexpr uint32_t kGradThreads = 256, kGradVectors = 4;  // of a piece: four vectors a thread
+static_assert(kGradThreads * kGradVectors * 16 == kGradPieceBytes, "a piece is one round of its threads");
 
 // What a thread gathers: sums of squares or of sizes, or the largest size, kept
 // as its bits (a NaN's are above every number's).
@@ -42,38 +42,141 @@ __device__ __forceinline__ double join(double a, double b) {
   return x > y ? a : b;  // sizes: their bits are in their order, a NaN's above
 }
 
-template <int NORM, int DT, uint32_t THREADS>
-__device__ __forceinline__ void gather(const GradPiece& p, Gather<NORM>& g) {
-  typedef Pack<DT, 16 / Width<DT>::bytes> V;
-  typedef Pack<DT, 1> One;
-  constexpr uint32_t VE = 16 / V::E;
-  const uint32_t vectors = p.count / VE;
-  u32x4 v[kGradVectors];
+// Addresses of eight of a tensor's other copies.
+struct Others {
+  unsigned char* copy[8];
+  __device__ __forceinline__ void load(const GradPiece& p, unsigned char* const* others, uint32_t from) {
+    if (p.copies < 2) return;
 #pragma unroll
-  for (uint32_t j = 0; j < kGradVectors; ++j) {
-    const uint32_t i = threadIdx.x + j * kGradThreads;
-    v[j] = i < vectors ? V::load(p.data + uint64_t(i) * 16) : u32x4{0, 0, 0, 0};
+    for (uint32_t k = 0; k < 8; ++k) copy[k] = others[p.first + min(from + k, p.copies - 2u)];
   }
-#pragma unroll
-  for (uint32_t j = 0; j < kGradVectors; ++j) {
-    float f[VE];
-    V::widen(v[j], f);
-#pragma unroll
-    for (uint32_t e = 0; e < VE; ++e) g.add(f[e]);
-  }
-  const uint32_t last = vectors * VE + threadIdx.x;
-  if (last < p.count) {
-    float f[1];
-    One::widen(One::load(p.data + uint64_t(last) * V::E), f);
-    g.add(f[0]);
-  }
-}
+};
 
-template <int NORM>
-__device__ __forceinline__ void gather(const GradPiece& p, Gather<NORM>& g) {
-  if (p.dtype == kF32) gather<NORM, kF32, kGradThreads>(p, g);
-  else if (p.dtype == kF16) gather<NORM, kF16, kGradThreads>(p, g);
-  else gather<NORM, kBF16, kGradThreads>(p, g);
+// A piece in the registers of the 256 threads `t` of it, as it lies in memory.
+struct Held {
+  u32x4 v[kGradVectors];
+  uint32_t single;  // of the few elements that fill no vector
+  template <int DT, bool STREAM>
+  __device__ __forceinline__ void load(const GradPiece& p, uint32_t t) {
+    typedef Pack<DT, 16 / Width<DT>::bytes> V;
+    constexpr uint32_t VE = 16 / V::E;
+    const uint32_t vectors = p.count / VE, last = vectors * VE + t;
+#pragma unroll
+    for (uint32_t j = 0; j < kGradVectors; ++j) {
+      const uint32_t i = t + j * kGradThreads;
+      v[j] = u32x4{0, 0, 0, 0};
+      if (i < vectors) v[j] = STREAM ? V::stream(p.data + uint64_t(i) * 16) : V::load(p.data + uint64_t(i) * 16);
+    }
+    single = 0;
+    if (last < p.count) single = Pack<DT, 1>::load(p.data + uint64_t(last) * V::E);
+  }
+  template <int DT, typename G>
+  __device__ __forceinline__ void gather(G& g) const {
+    typedef Pack<DT, 16 / Width<DT>::bytes> V;
+    constexpr uint32_t VE = 16 / V::E;
+    float f[VE], one[1];
+#pragma unroll
+    for (uint32_t j = 0; j < kGradVectors; ++j) {
+      V::widen(v[j], f);
+#pragma unroll
+      for (uint32_t e = 0; e < VE; ++e) g.add(f[e]);
+    }
+    Pack<DT, 1>::widen(single, one);
+    g.add(one[0]);
+  }
+  template <int DT>
+  __device__ __forceinline__ void scale(float factor) {
+    typedef Pack<DT, 16 / Width<DT>::bytes> V;
+    constexpr uint32_t VE = 16 / V::E;
+    float f[VE], one[1];
+#pragma unroll
+    for (uint32_t j = 0; j < kGradVectors; ++j) {
+      V::widen(v[j], f);
+#pragma unroll
+      for (uint32_t e = 0; e < VE; ++e) f[e] *= factor;
+      v[j] = V::narrow(f);
+    }
+    Pack<DT, 1>::widen(single, one);
+    one[0] *= factor;
+    single = Pack<DT, 1>::narrow(one);
+  }
+  template <int DT, bool STREAM>
+  __device__ __forceinline__ void store(unsigned char* to, uint32_t count, uint32_t t) const {
+    typedef Pack<DT, 16 / Width<DT>::bytes> V;
+    constexpr uint32_t VE = 16 / V::E;
+    const uint32_t vectors = count / VE, last = vectors * VE + t;
+#pragma unroll
+    for (uint32_t j = 0; j < kGradVectors; ++j) {
+      const uint32_t i = t + j * kGradThreads;
+      if (i >= vectors) continue;
+      if constexpr (STREAM) V::store_nt(to + uint64_t(i) * 16, v[j]);
+      else V::store(to + uint64_t(i) * 16, v[j]);
+    }
+    if (last < count) Pack<DT, 1>::store(to + uint64_t(last) * V::E, single);
+  }
+  // To a copy at another phase of 16 bytes than the piece, which lies in `lds`: its
+  // vectors are put together there, since stores that cross 16 bytes are slow (8
+  // copies of 48 million bf16 gradients, seven of them so: 234 us, and 185 so).
+  template <int DT, bool STREAM>
+  static __device__ __forceinline__ void store_shifted(unsigned char* to, const uint32_t* lds, uint32_t count, uint32_t t) {
+    typedef Pack<DT, 16 / Width<DT>::bytes> V;
+    constexpr uint32_t E = V::E, VE = 16 / E;
+    const uint32_t head = min(count, (128 - (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to)) & 127)) % 128 / E);
+    const uint32_t vectors = (count - head) / VE, tail = head + vectors * VE;
+#pragma unroll
+    for (uint32_t j = 0; j < kGradVectors; ++j) {
+      const uint32_t i = t + j * kGradThreads;
+      if (i >= vectors) continue;
+      const uint32_t at = head * E + i * 16, turn = at % 4 * 8;
+      uint32_t w[5];
+      u32x4 r;
+#pragma unroll
+      for (uint32_t k = 0; k < 5; ++k) w[k] = lds[at / 4 + k];
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) r[k] = __builtin_amdgcn_alignbit(w[k + 1], w[k], turn);
+      if constexpr (STREAM) V::store_nt(to + at, r);
+      else V::store(to + at, r);
+    }
+    uint32_t c = t;
+    if (c >= head) c += tail - head;
+    if (c < count) Pack<DT, 1>::store(to + uint64_t(c) * E, Pack<DT, 1>::load(reinterpret_cast<const unsigned char*>(lds) + c * E));
+  }
+  // To every copy of the piece, eight of their addresses at a time, the first of them
+  // in `to`.  With `lds`, by way of it where a copy lies at another phase (p.shifted:
+  // any does).
+  template <int DT, bool STREAM>
+  __device__ __forceinline__ void store_all(const GradPiece& p, unsigned char* const* others, uint32_t t, uint32_t* lds, Others to) const {
+    constexpr uint32_t E = Width<DT>::bytes, VE = 16 / E;
+    if (lds && p.shifted) {
+      const uint32_t vectors = p.count / VE, last = vectors * VE + t;
+#pragma unroll
+      for (uint32_t j = 0; j < kGradVectors; ++j) {
+        const uint32_t i = t + j * kGradThreads;
+        if (i < vectors) *reinterpret_cast<u32x4*>(lds + i * 4) = v[j];
+      }
+      if (last < p.count) Pack<DT, 1>::store(reinterpret_cast<unsigned char*>(lds) + last * E, single);
+      __syncthreads();
+    }
+    store<DT, STREAM>(p.data, p.count, t);
+    for (uint32_t c = 0; c + 1 < p.copies; c += 8) {
+      if (c > 0) to.load(p, others, c);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        if (c + k + 1 >= p.copies) continue;
+        unsigned char* const at = to.copy[k] + p.offset;
+        if (lds && ((reinterpret_cast<uintptr_t>(at) ^ reinterpret_cast<uintptr_t>(p.data)) & 127) != 0) store_shifted<DT, STREAM>(at, lds, p.count, t);
+        else store<DT, STREAM>(at, p.count, t);
+      }
+    }
+  }
+};
+
+// f(type) for the piece's type.
+template <typename F>
+__device__ __forceinline__ void by_type(uint32_t dtype, F&& f) {
+  if (dtype == kF32) f(std::integral_constant<int, kF32>{});
+  else if (dtype == kF16) f(std::integral_constant<int, kF16>{});
+  else f(std::integral_constant<int, kBF16>{});
 }
 
 // The workgroup's values joined, in every thread.
@@ -98,95 +201,119 @@ __device__ __forceinline__ float factor_of(const GradArgs& a, double total, bool
   return static_cast<float>(a.scale * clip);
 }
 
-template <int DT, bool STREAM>
-__device__ __forceinline__ void scale(const GradPiece& p, unsigned char* const* others, float factor) {
-  typedef Pack<DT, 16 / Width<DT>::bytes> V;
-  typedef Pack<DT, 1> One;
-  constexpr uint32_t VE = 16 / V::E;
-  const uint32_t vectors = p.count / VE;
-  u32x4 v[kGradVectors];
-#pragma unroll
-  for (uint32_t j = 0; j < kGradVectors; ++j) {
-    const uint32_t i = threadIdx.x + j * kGradThreads;
-    if (i < vectors) v[j] = V::load(p.data + uint64_t(i) * 16);
-  }
-  const uint32_t last = vectors * VE + threadIdx.x;
-  uint32_t single = 0;
-  if (last < p.count) single = One::load(p.data + uint64_t(last) * V::E);
-#pragma unroll
-  for (uint32_t j = 0; j < kGradVectors; ++j) {
-    float f[VE];
-    V::widen(v[j], f);
-#pragma unroll
-    for (uint32_t e = 0; e < VE; ++e) f[e] *= factor;
-    v[j] = V::narrow(f);
-  }
-  float f[1];
-  One::widen(single, f);
-  f[0] *= factor;
-  single = One::narrow(f);
-  for (uint32_t c = 0; c < p.copies; ++c) {
-    unsigned char* to = c == 0 ? p.data : others[p.first + c - 1] + p.offset;
-#pragma unroll
-    for (uint32_t j = 0; j < kGradVectors; ++j) {
-      const uint32_t i = threadIdx.x + j * kGradThreads;
-      if (i < vectors) {
-        if constexpr (STREAM) V::store_nt(to + uint64_t(i) * 16, v[j]);
-        else V::store(to + uint64_t(i) * 16, v[j]);
-      }
-    }
-    if (last < p.count) One::store(to + uint64_t(last) * V::E, single);
-  }
-}
-
-template <bool STREAM>
-__device__ __forceinline__ void scale(const GradPiece& p, unsigned char* const* others, float factor) {
-  if (p.dtype == kF32) scale<kF32, STREAM>(p, others, factor);
-  else if (p.dtype == kF16) scale<kF16, STREAM>(p, others, factor);
-  else scale<kBF16, STREAM>(p, others, factor);
-}
-
-// One partial sum a workgroup, over every gridDim.x-th piece.
-template <int NORM>
+// One partial sum a workgroup, over every gridDim.x-th piece, whose record is on
+// its way while the piece before is read.
+template <int NORM, bool STREAM>
 __global__ __launch_bounds__(kGradThreads) void grad_gather(GradArgs a) {
   __shared__ double shared[kGradThreads / 64];
   Gather<NORM> g;
-  for (uint32_t i = blockIdx.x; i < a.n; i += gridDim.x) gather(a.pieces[i], g);
+  GradPiece next = a.pieces[blockIdx.x];
+  for (uint32_t i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const GradPiece p = next;
+    if (i + gridDim.x < a.n) next = a.pieces[i + gridDim.x];
+    by_type(p.dtype, [&](auto type) {
+      Held h;
+      h.load<decltype(type)::value, STREAM>(p, threadIdx.x);
+      h.gather<decltype(type)::value>(g);
+    });
+  }
   const double x = join_workgroup<NORM>(g.value(), shared);
   if (threadIdx.x == 0) a.partial[blockIdx.x] = x;
 }
 
-// The partial sums joined, then (with a.clip) the pieces scaled, last pieces
-// first: what the gathering launch read last may still be cached.
-template <int NORM, bool STREAM>
-__global__ __launch_bounds__(kGradThreads) void grad_scale(GradArgs a) {
-  __shared__ double shared[kGradThreads / 64];
+// The partial sums joined, in every thread.
+template <int NORM>
+__device__ __forceinline__ double join_partial(const GradArgs& a, double* shared) {
   double x = 0.0;
   for (uint32_t i = threadIdx.x; i < a.sums; i += kGradThreads) x = join<NORM>(x, a.partial[i]);
-  x = join_workgroup<NORM>(x, shared);
-  const float factor = factor_of<NORM>(a, x, blockIdx.x == 0 && threadIdx.x == 0);
-  if (!a.clip || factor == 1.0f) return;
-  for (uint32_t i = blockIdx.x; i < a.n; i += gridDim.x) scale<STREAM>(a.pieces[a.n - 1 - i], a.others, factor);
+  return join_workgroup<NORM>(x, shared);
 }
 
-// Few pieces: one workgroup, one launch, nothing kept.
+// The norm, and the factor to where the partial sums end.
 template <int NORM>
-__global__ __launch_bounds__(kGradThreads) void grad_few(GradArgs a) {
+__global__ __launch_bounds__(kGradThreads) void grad_factor(GradArgs a) {
   __shared__ double shared[kGradThreads / 64];
+  const float factor = factor_of<NORM>(a, join_partial<NORM>(a, shared), threadIdx.x == 0);
+  if (threadIdx.x == 0) *reinterpret_cast<float*>(a.partial + a.sums) = factor;
+}
+
+// The pieces scaled, a workgroup each.  FACTOR: by the factor that grad_factor left;
+// else (few pieces) every workgroup joins the partial sums itself, while its piece
+// is read.  Last pieces first: what was gathered last may still be cached.
+template <int NORM, bool FACTOR, bool STREAM>
+__global__ __launch_bounds__(kGradThreads) void grad_scale(GradArgs a) {
+  __shared__ double shared[kGradThreads / 64];
+  __shared__ __attribute__((aligned(16))) uint32_t lds[kGradPieceBytes / 4 + 4];
+  const GradPiece p = a.pieces[a.n - 1 - blockIdx.x];
+  float factor = 1.0f;
+  if constexpr (FACTOR) {
+    factor = *reinterpret_cast<const float*>(a.partial + a.sums);
+    if (factor == 1.0f) return;
+  }
+  by_type(p.dtype, [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+    Held h;
+    Others to;
+    h.load<DT, STREAM>(p, threadIdx.x);
+    to.load(p, a.others, 0);
+    if constexpr (!FACTOR) factor = factor_of<NORM>(a, join_partial<NORM>(a, shared), blockIdx.x == 0 && threadIdx.x == 0);
+    if (factor == 1.0f) return;
+    h.scale<DT>(factor);
+    h.store_all<DT, STREAM>(p, a.others, threadIdx.x, lds, to);
+  });
+}
+
+// Few pieces: one workgroup of four groups of 256 threads holds them, so that they
+// are read once, by one launch.
+constexpr uint32_t kFewGroups = 4, kFewRounds = 2;
+
+template <int NORM>
+__global__ __launch_bounds__(kGradThreads * kFewGroups) void grad_few(GradArgs a) {
+  __shared__ double shared[kGradThreads * kFewGroups / 64];
+  const uint32_t group = uniform(threadIdx.x / kGradThreads), t = threadIdx.x % kGradThreads;
   Gather<NORM> g;
-  for (uint32_t i = 0; i < a.n; ++i) gather(a.pieces[i], g);
+  Held h[kFewRounds];
+#pragma unroll
+  for (uint32_t r = 0; r < kFewRounds; ++r)
+    if (group + r * kFewGroups < a.n) {
+      const GradPiece p = a.pieces[group + r * kFewGroups];
+      by_type(p.dtype, [&](auto type) { h[r].template load<decltype(type)::value, false>(p, t); });
+    }
+#pragma unroll
+  for (uint32_t r = 0; r < kFewRounds; ++r)
+    if (group + r * kFewGroups < a.n)
+      by_type(a.pieces[group + r * kFewGroups].dtype, [&](auto type) { h[r].template gather<decltype(type)::value>(g); });
   const double x = join_workgroup<NORM>(g.value(), shared);
   const float factor = factor_of<NORM>(a, x, threadIdx.x == 0);
   if (!a.clip || factor == 1.0f) return;
-  for (uint32_t i = 0; i < a.n; ++i) scale<false>(a.pieces[i], a.others, factor);
+#pragma unroll
+  for (uint32_t r = 0; r < kFewRounds; ++r)
+    if (group + r * kFewGroups < a.n) {
+      const GradPiece p = a.pieces[group + r * kFewGroups];
+      by_type(p.dtype, [&](auto type) {
+        Others to;
+        to.load(p, a.others, 0);
+        h[r].template scale<decltype(type)::value>(factor);
+        h[r].template store_all<decltype(type)::value, false>(p, a.others, t, nullptr, to);
+      });
+    }
 }
 
 }  // namespace dev
 
-constexpr uint32_t kGradGroups = 2048, kGradFew = 4;
+namespace {
 
-uint32_t grad_sums(uint64_t pieces) {
-  return pieces <= kGradFew ? 0 : static_cast<uint32_t>(std::min<uint64_t>(pieces, kGradGroups));
+constexpr uint32_t kGradGroups = 2048;      // of the gathering launch at most: eight a compute unit
+constexpr uint32_t kGradJoined = 1024;      // pieces up to which every scaling workgroup joins the sums
+constexpr uint64_t kGradFewBytes = 128 << 10;  // written by one workgroup at most
+constexpr uint64_t kGradCached = uint64_t(256) << 20;  // the memory-side cache
+
+bool few(uint64_t pieces, uint64_t written) { return pieces <= dev::kFewGroups * dev::kFewRounds && written <= kGradFewBytes; }
+
+}  // namespace
+
+uint32_t grad_sums(uint64_t pieces, uint64_t written) {
+  return few(pieces, written) ? 0 : static_cast<uint32_t>(std::min<uint64_t>(pieces, kGradGroups));
 }
 
 namespace {
@@ -194,15 +321,22 @@ namespace {
 template <int NORM>
 hipError_t launch(const GradArgs& a, hipStream_t stream) {
   if (a.sums == 0) {
-    dev::grad_few<NORM><<<1, dev::kGradThreads, 0, stream>>>(a);
+    dev::grad_few<NORM><<<1, dev::kGradThreads * dev::kFewGroups, 0, stream>>>(a);
     return hipGetLastError();
   }
-  dev::grad_gather<NORM><<<a.sums, dev::kGradThreads, 0, stream>>>(a);
-  const hipError_t e = hipGetLastError();
+  if (a.read > kGradCached) dev::grad_gather<NORM, true><<<a.sums, dev::kGradThreads, 0, stream>>>(a);
+  else dev::grad_gather<NORM, false><<<a.sums, dev::kGradThreads, 0, stream>>>(a);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const uint32_t groups = a.clip ? std::min(a.n, kGradGroups) : 1;
-  if (a.stream) dev::grad_scale<NORM, true><<<groups, dev::kGradThreads, 0, stream>>>(a);
-  else dev::grad_scale<NORM, false><<<groups, dev::kGradThreads, 0, stream>>>(a);
+  if (a.clip && a.n <= kGradJoined) {
+    dev::grad_scale<NORM, false, false><<<a.n, dev::kGradThreads, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  dev::grad_factor<NORM><<<1, dev::kGradThreads, 0, stream>>>(a);
+  e = hipGetLastError();
+  if (e != hipSuccess || !a.clip) return e;
+  if (a.written >= kStreamBytes) dev::grad_scale<0, true, true><<<a.n, dev::kGradThreads, 0, stream>>>(a);
+  else dev::grad_scale<0, true, false><<<a.n, dev::kGradThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -16,7 +16,7 @@ using namespace hbmc;
 struct hbmc_gradients {
   int device = -1;
   uint32_t pieces = 0;
-  uint64_t written = 0;  // bytes that a clipping call writes
+  uint64_t read = 0, written = 0;  // bytes of the tensors, of all their copies
   std::vector<std::pair<uintptr_t, uintptr_t>> held;  // the gradients' memory, ascending
   void* table = nullptr;
   const GradPiece* piece = nullptr;
@@ -46,10 +46,13 @@ hbmc_status_t create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t t[], hbmc
       g->held.emplace_back(at, at + bytes);
     }
     if (r.bad()) return HBMC_ERR_INVALID_ARG;
+    g->read += bytes;
     g->written += bytes * static_cast<uint64_t>(t[i].copies);
     GradPiece p = {};
     p.dtype = static_cast<uint32_t>(t[i].dtype);
-    p.copies = static_cast<uint32_t>(t[i].copies);
+    p.copies = static_cast<uint16_t>(t[i].copies);
+    for (int c = 1; c < t[i].copies; ++c)
+      if ((reinterpret_cast<uintptr_t>(t[i].data[c]) ^ reinterpret_cast<uintptr_t>(t[i].data[0])) & 127) p.shifted = 1;
     p.first = static_cast<uint32_t>(others.size());
     if (others.size() + static_cast<size_t>(P) > UINT32_MAX) return HBMC_ERR_UNSUPPORTED;
     for (int c = 1; c < t[i].copies; ++c) others.push_back(static_cast<unsigned char*>(t[i].data[c]));
@@ -66,7 +69,7 @@ hbmc_status_t create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t t[], hbmc
       at += here;
       most = kGradPieceBytes;
     }
-    if (pieces.size() > (size_t(1) << 31)) return HBMC_ERR_UNSUPPORTED;
+    if (pieces.size() > kMaxGradPieces) return HBMC_ERR_UNSUPPORTED;
   }
   if (!r.ok()) return HBMC_ERR_INVALID_ARG;
   std::sort(g->held.begin(), g->held.end());
@@ -88,6 +91,12 @@ hbmc_status_t create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t t[], hbmc
   return HBMC_OK;
 }
 
+// Bytes of the partial sums and the factor.
+uint64_t workspace_of(const hbmc_gradients* g) {
+  const uint32_t sums = grad_sums(g->pieces, g->written);
+  return sums ? (uint64_t(sums) + 1) * sizeof(double) : 0;
+}
+
 // Whether [p, p + bytes) is apart from every gradient and from the table.
 bool apart(const hbmc_gradients* g, const void* p, uint64_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
@@ -102,8 +111,8 @@ hbmc_status_t run(const hbmc_gradients* g, double norm_type, double scale, bool 
       (clip && (!(max_norm >= 0.0) || !(eps >= 0.0) || !std::isfinite(eps))))
     return HBMC_ERR_INVALID_ARG;
   GradArgs a = {};
-  a.sums = grad_sums(g->pieces);
-  const uint64_t bytes = uint64_t(a.sums) * sizeof(double);
+  a.sums = grad_sums(g->pieces, g->written);
+  const uint64_t bytes = workspace_of(g);
   if (workspace_bytes < bytes) return HBMC_ERR_INVALID_ARG;
   Ranges r;
   r.write(norm, 4, 4);
@@ -117,7 +126,8 @@ hbmc_status_t run(const hbmc_gradients* g, double norm_type, double scale, bool 
   a.n = g->pieces;
   a.norm = norm_type == 2.0 ? 2 : norm_type == 1.0 ? 1 : 0;
   a.clip = clip;
-  a.stream = g->written >= kStreamBytes;
+  a.read = g->read;
+  a.written = g->written;
   a.scale = scale;
   a.max_norm = max_norm;
   a.eps = eps;
@@ -149,7 +159,7 @@ hbmc_status_t hbmc_gradients_destroy(hbmc_gradients_t g) {
 
 hbmc_status_t hbmc_gradients_workspace(hbmc_gradients_t g, size_t* bytes) {
   if (!g || !bytes) return HBMC_ERR_INVALID_ARG;
-  *bytes = grad_sums(g->pieces) * sizeof(double);
+  *bytes = workspace_of(g);
   return HBMC_OK;
 }
 

@@ -149,7 +149,8 @@ struct GradPiece {
   uint32_t count;   // elements
   uint32_t dtype;
   uint32_t first;   // of the other copies' addresses
-  uint32_t copies;  // buffers that hold the tensor, `data`'s included
+  uint16_t copies;  // buffers that hold the tensor, `data`'s included
+  uint16_t shifted; // whether any lies at another phase of 16 bytes
 };
 
 struct GradArgs {
@@ -159,14 +160,16 @@ struct GradArgs {
   uint32_t sums;  // partial sums in `partial`
   int norm;       // 1, 2, or 0 for the largest value
   bool clip;      // whether the gradients are scaled
-  bool stream;    // stores past the memory-side cache
+  uint64_t read, written;  // bytes of the tensors, of all their copies
   double scale, max_norm, eps;
   double* partial;
   float* norm_out;
 };
 
 constexpr uint64_t kGradPieceBytes = uint64_t(16) << 10;
-uint32_t grad_sums(uint64_t pieces);  // partial sums of so many pieces (0: none are kept)
+constexpr uint64_t kMaxGradPieces = uint64_t(1) << 23;  // a workgroup each: below 2^32 threads
+// Partial sums of so many pieces, whose copies hold `written` bytes (0: none are kept).
+uint32_t grad_sums(uint64_t pieces, uint64_t written);
 hipError_t launch_grad(const GradArgs& a, hipStream_t stream);
 
 // ------------------------------------ penalties, biases and masks on logits

@@ -744,7 +744,8 @@ hbmc_status_t hbmc_product(hbmc_comm_t comm, const hbmc_product_t* prod, const i
  * reduce-scatter dealt out, a dealt-out weight's gradient), or one on each of the
  * P ranks that hold the same values (as an AllReduce leaves them): data[0]'s are
  * read, and every buffer is written from them.  Tensors of several types may be
- * mixed; buffers of a handle must not overlap.  The handle does not need the
+ * mixed; buffers of a handle must not overlap, and hold at most 2^23 pieces of 16
+ * KiB in all, copies not counted (HBMC_ERR_UNSUPPORTED).  The handle does not need the
  * communicator afterwards, works on the device current at its creation (else
  * HBMC_ERR_INVALID_ARG), and must outlive graphs that hold its calls.
  */

@@ -290,3 +290,45 @@ def test_past_32_bit_offsets():
         g.clip(6.5, out, eps=0.0)
     assert float(out) == 13.0 and float(t[n - 1]) == 2.0 and float(t[1 << 30]) == 6.0 and float(t[5]) == 1.5
     assert int((t != 0).sum()) == 3
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF])
+@pytest.mark.parametrize("P", [2, 3, 12])
+@pytest.mark.parametrize("lengths", [[1 << 18, 65537, 3, 0, 129], [33, 1]])
+def test_copies_at_every_phase(P, lengths, dtype):
+    """Copy after copy one element further from 128 bytes, packed tensor behind tensor, with guards."""
+    host = made(lengths, (dtype,), P)
+    total = sum(lengths)
+    flats = [torch.full((total + 300,), 7, dtype=dtype, device="cuda") for _ in range(P)]
+    copies = []
+    for r, flat in enumerate(flats):
+        at = 100 + 5 * r
+        copies.append(list(flat[at:at + total].split(lengths)))
+        if r == 0:
+            for t, h in zip(copies[0], host):
+                t.copy_(h)
+    out = number()
+    size = step.norm(host, 2.0, 0.25)
+    with hc.Comm(P, "ring") as c, c.gradients(same=copies) as g:
+        g.clip(float(size) / 2, out, scale=0.25, eps=0.0)
+    near(out, size)
+    by = step.factor(size, float(size) / 2, 0.25, 0.0)
+    for r, flat in enumerate(flats):
+        for t, h in zip(copies[r], host):
+            ref.check(t, (h.double() * by, h.double().abs() * by), 2, "gradient")
+        at = 100 + 5 * r
+        assert bool((flat[:at] == 7).all()) and bool((flat[at + total:] == 7).all())
+
+
+@pytest.mark.parametrize("pieces", [1, 4, 5, 8, 9, 1023, 1024, 1025, 2048, 2049, 5000])
+def test_each_way_of_launching(pieces):
+    n = pieces * 4096 - 3
+    t, out = torch.full((n,), 0.5, device="cuda"), number()
+    host = torch.full((n,), 0.5)
+    with hc.Comm(1, "ring") as c, c.gradients(dealt=[[t]]) as g:
+        size = step.norm([host], 2.0)
+        g.norm(out)
+        near(out, size)
+        g.clip(float(size) / 8, out, eps=0.0)
+        near(out, size)
+    ref.check(t.cpu(), (torch.full((n,), 0.0625).double(), torch.full((n,), 0.0625).double()), 2, "gradient")
