@@ -630,38 +630,11 @@ class Gradients:
     fp32, fp16 or bf16 in any mixture, and do not overlap."""
 
     def __init__(self, comm: Comm, dealt=None, same=None):
-        import torch
         self._h = ctypes.c_void_p()
-        dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-
-        def address(t, like):
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"gradients are tensors, got {type(t).__name__}")
-            if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
-                raise ValueError(f"a contiguous tensor on device {dev} is needed, got one on {t.device}")
-            if t.dtype != like.dtype or t.shape != like.shape:
-                raise ValueError("a tensor of `same` has one type and shape on every rank")
-            return t.data_ptr()
-
-        groups = [(t,) for mine in self._ranks(comm, dealt, "dealt") for t in mine]
-        copies = self._ranks(comm, same, "same")
-        if any(len(mine) != len(copies[0]) for mine in copies):
-            raise ValueError("same: every rank holds the same tensors")
-        groups += zip(*copies)
-        table = (Gradient * max(1, len(groups)))()
-        for g, held in zip(table, groups):
-            g.data = (ctypes.c_void_p * len(held))(*[address(t, held[0]) for t in held])
-            g.count, g.dtype, g.copies = held[0].numel(), DTYPE[_torch_dtype_name(held[0])], len(held)
-        _check(load_library().hbmc_gradients_create(comm._h, len(groups), table, ctypes.byref(self._h)),
-               "hbmc_gradients_create")
-        self._keep = groups  # the gradients' memory stays with the handle
-
-    @staticmethod
-    def _ranks(comm, lists, what):
-        lists = [[]] * comm.P if lists is None else [list(mine) for mine in lists]
-        if len(lists) != comm.P:
-            raise ValueError(f"{what}: a list of tensors for each of {comm.P} ranks is needed, got {len(lists)}")
-        return lists
+        self._keep = [[list(mine) for mine in lists] if lists is not None else None for lists in (dealt, same)]
+        rc, handle = load_operators().create_gradients(comm._h.value or 0, comm.P, _current_device(), *self._keep)
+        _check(rc, "hbmc_gradients_create")
+        self._h = ctypes.c_void_p(handle)  # _keep: the gradients' memory stays with the handle
 
     def _call(self, name, stream, *args):
         dev = _current_device()

@@ -530,16 +530,101 @@ hbmc_status_t gradients_call(PyObject* const* a, bool clip, PyObject* alloc) {
 hbmc_status_t gradients_norm(PyObject* const* a) { return gradients_call(a, false, a[6]); }
 hbmc_status_t gradients_clip(PyObject* const* a) { return gradients_call(a, true, a[8]); }
 
+// Lists of tensors, one for each of P ranks (NULL: none at all).
+struct TensorLists {
+  std::vector<std::vector<const at::Tensor*>> ranks;
+  TensorLists(PyObject* o, int P, const char* what) : ranks(static_cast<size_t>(P)) {
+    if (o == Py_None) return;
+    PyObject* const outer = PySequence_Fast(o, "a list of the ranks' lists of tensors is needed");
+    if (!outer) throw Raised();
+    held_.push_back(outer);
+    if (PySequence_Fast_GET_SIZE(outer) != P)
+      raise_freed(PyExc_ValueError, "%s: a list of tensors for each of %d ranks is needed, got %d", what, P,
+                  static_cast<int>(PySequence_Fast_GET_SIZE(outer)));
+    for (int r = 0; r < P; ++r) {
+      PyObject* const inner = PySequence_Fast(PySequence_Fast_GET_ITEM(outer, r), "a list of tensors is needed for each rank");
+      if (!inner) {
+        release();
+        throw Raised();
+      }
+      held_.push_back(inner);
+      for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(inner); ++i) {
+        PyObject* const item = PySequence_Fast_GET_ITEM(inner, i);
+        if (!THPVariable_Check(item)) raise_freed(PyExc_TypeError, "%s: tensors are needed, got %.80s", what, Py_TYPE(item)->tp_name);
+        ranks[static_cast<size_t>(r)].push_back(&THPVariable_Unpack(item));
+      }
+    }
+  }
+  ~TensorLists() { release(); }
+  TensorLists(const TensorLists&) = delete;
+  TensorLists& operator=(const TensorLists&) = delete;
+
+ private:
+  template <typename... A>
+  [[noreturn]] void raise_freed(PyObject* type, const char* format, A... a) {
+    PyErr_Format(type, format, a...);
+    release();
+    throw Raised();
+  }
+  void release() {
+    for (PyObject* o : held_) Py_DECREF(o);
+    held_.clear();
+  }
+  std::vector<PyObject*> held_;
+};
+
+// A gradients' handle: (comm handle, P, device, dealt, same) -> (status, handle).
+PyObject* create_gradients(PyObject* const* a) {
+  const hbmc_comm_t comm = static_cast<hbmc_comm_t>(pointer(a[0]));
+  const int P = static_cast<int>(integer(a[1])), dev = static_cast<int>(integer(a[2]));
+  if (P < 1 || P > kMaxRanks) raise(PyExc_ValueError, "%d ranks", P);
+  const TensorLists dealt(a[3], P, "dealt"), same(a[4], P, "same");
+  std::vector<hbmc_gradient_t> table;
+  std::vector<void*> addresses;
+  const auto add = [&](const at::Tensor& t, const at::Tensor& like) {
+    if (t.get_device() != dev || !t.is_contiguous())
+      raise(PyExc_ValueError, "gradients: a contiguous tensor on device %d is needed, got %sone on device %d", dev,
+            t.is_contiguous() ? "" : "a non-contiguous ", static_cast<int>(t.get_device()));
+    if (t.scalar_type() != like.scalar_type() || t.sizes() != like.sizes())
+      raise(PyExc_ValueError, "gradients: a tensor of `same` has one type and shape on every rank");
+    addresses.push_back(t.numel() ? t.data_ptr() : nullptr);
+  };
+  for (const auto& mine : dealt.ranks)
+    for (const at::Tensor* t : mine) {
+      table.push_back({static_cast<size_t>(t->numel()), static_cast<hbmc_dtype_t>(dtype_code(*t, "gradients")), 1, nullptr});
+      add(*t, *t);
+    }
+  const size_t n = same.ranks[0].size();
+  for (const auto& mine : same.ranks)
+    if (mine.size() != n) raise(PyExc_ValueError, "same: every rank holds the same tensors");
+  for (size_t i = 0; i < n; ++i) {
+    const at::Tensor& first = *same.ranks[0][i];
+    table.push_back({static_cast<size_t>(first.numel()), static_cast<hbmc_dtype_t>(dtype_code(first, "gradients")), P, nullptr});
+    for (int r = 0; r < P; ++r) add(*same.ranks[static_cast<size_t>(r)][i], first);
+  }
+  size_t at = 0;
+  for (hbmc_gradient_t& g : table) {
+    g.data = addresses.data() + at;
+    at += static_cast<size_t>(g.copies);
+  }
+  hbmc_gradients_t g = nullptr;
+  const hbmc_status_t st = hbmc_gradients_create(comm, table.size(), table.data(), &g);
+  return Py_BuildValue("iN", static_cast<int>(st), PyLong_FromVoidPtr(g));
+}
+
 // Entry of one function: its number of arguments, the status it returns, and no
 // C++ exception past it.
-template <hbmc_status_t (*F)(PyObject* const*), Py_ssize_t N>
+PyObject* result(hbmc_status_t s) { return PyLong_FromLong(s); }
+PyObject* result(PyObject* o) { return o; }
+
+template <auto F, Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
     PyErr_Format(PyExc_TypeError, "%zd arguments are needed, got %zd", N, n);
     return nullptr;
   }
   try {
-    return PyLong_FromLong(F(args));
+    return result(F(args));
   } catch (const Raised&) {
     return nullptr;
   } catch (const std::exception& e) {
@@ -548,7 +633,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
 }
 
-template <hbmc_status_t (*F)(PyObject* const*), Py_ssize_t N>
+template <auto F, Py_ssize_t N>
 constexpr PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
@@ -562,6 +647,7 @@ PyMethodDef methods[] = {method<reduce_norm, 15>("reduce_norm"),
                          method<adjust_logits, 15>("adjust_logits"),
                          method<quantize_rows, 7>("quantize_rows"),
                          method<product, 10>("product"),
+                         method<create_gradients, 5>("create_gradients"),
                          method<gradients_norm, 7>("gradients_norm"),
                          method<gradients_clip, 9>("gradients_clip"),
                          {nullptr, nullptr, 0, nullptr}};
