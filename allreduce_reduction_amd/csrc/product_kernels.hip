@@ -144,12 +144,22 @@ __device__ __forceinline__ i32x4 keep_from(i32x4 v, uint32_t first) {  // zeros 
   }
   return v;
 }
-// Where a rank has rows of fewer than 16 codes, all go one by one.
-__device__ __forceinline__ i32x4 short_row(const unsigned char* row, uint32_t n, uint32_t k) {
+// 16 codes of row r from position k, one by one, zeros past the `inner` ones: where a
+// rank has rows of fewer than 16.  For a sum over the ranks `inner` is all of them's,
+// rank after rank, so that many ranks with few codes take one stage and not one each.
+__device__ __forceinline__ i32x4 short_chunk(const ProductArgs& a, const unsigned char* const* ranks, uint64_t r, uint32_t rank, uint32_t inner,
+                                             uint32_t k) {
   i32x4 v = {0, 0, 0, 0};
+  const uint32_t each = a.form >= 2 ? a.inner_seg : inner;
+  uint32_t q = a.form >= 2 ? k / each : rank, off = a.form >= 2 ? k % each : k;
 #pragma unroll
-  for (uint32_t i = 0; i < 16; ++i)
-    if (k + i < n) v[i / 4] |= static_cast<int32_t>(static_cast<uint32_t>(row[k + i]) << (8 * (i % 4)));
+  for (uint32_t i = 0; i < 16; ++i) {
+    if (k + i >= inner) continue;
+    const uint32_t n = a.form >= 2 ? min(each, a.inner - q * each) : inner;
+    v[i / 4] |= static_cast<int32_t>(static_cast<uint32_t>(ranks[q][r * n + off]) << (8 * (i % 4)));
+    if (a.form >= 2 && ++off == each) off = 0, ++q;
+    else if (a.form < 2) ++off;
+  }
   return v;
 }
 
@@ -192,11 +202,75 @@ __device__ __forceinline__ void store_results(const ProductArgs& a, uint32_t own
   }
 }
 
+// A wave's 16 * FT tokens from t0 by 16 * FN channels from n0.  They go through its
+// SHARE bytes of LDS, so that rows of its channels are stored whole (128 bytes and
+// more of a 256 by 256 tile's; 4096 x 4096 results of 8192 codes 118 us without, 108
+// so, to 8 ranks 271 and 147).
+template <int DT, uint32_t FT, uint32_t FN, uint32_t SHARE>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, uint32_t own, uint32_t channels, uint32_t t0, uint32_t n0,
+                                           const i32x4 (&acc)[FT][FN], unsigned char* mine, uint32_t lane) {
+  typedef Pack<DT, 16 / Width<DT>::bytes> V;
+  typedef Pack<DT, 1> One;
+  constexpr uint32_t E = V::E, VE = 16 / E, NW = FN * 16, PITCH = NW * E + 16;
+  constexpr uint32_t FITS = SHARE / PITCH / 16, BATCH = FITS >= FT ? FT : FITS >= FT / 2 ? FT / 2 : FITS >= FT / 4 ? FT / 4 : 1;
+  static_assert(FITS >= 1 && FT % BATCH == 0, "a batch of 16 rows at least");
+#pragma unroll
+  for (uint32_t i0 = 0; i0 < FT; i0 += BATCH) {
+#pragma unroll
+    for (uint32_t i = i0; i < i0 + BATCH; ++i) {
+      const uint32_t t = t0 + i * 16 + lane % 16;
+      const float xs = a.x_scale[min(t, a.rows - 1)];
+#pragma unroll
+      for (uint32_t j = 0; j < FN; ++j) {
+        const uint32_t n = j * 16 + lane / 16 * 4;
+        float f[4];
+#pragma unroll
+        for (uint32_t e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i][j][e]) * xs * a.w_scale[own][min(n0 + n + e, channels - 1)];
+        unsigned char* const to = mine + ((i - i0) * 16 + lane % 16) * PITCH + n * E;
+        if constexpr (DT == kF32) *reinterpret_cast<u32x4*>(to) = u32x4{f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3])};
+        else *reinterpret_cast<u32x2*>(to) = u32x2{Pack<DT, 8>::narrow2(f[0], f[1]), Pack<DT, 8>::narrow2(f[2], f[3])};
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr uint32_t CHUNKS_ROW = NW * E / 16;
+#pragma unroll
+    for (uint32_t c0 = 0; c0 < BATCH * 16 * CHUNKS_ROW; c0 += 64) {
+      const uint32_t c = c0 + lane, r = c / CHUNKS_ROW, n = n0 + c % CHUNKS_ROW * VE, t = t0 + i0 * 16 + r;
+      if (c0 + 64 > BATCH * 16 * CHUNKS_ROW && c >= BATCH * 16 * CHUNKS_ROW) continue;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c % CHUNKS_ROW * 16);
+      if (t >= a.rows || n >= channels) continue;
+      const uint32_t left_n = channels - n;
+      const auto put = [&](unsigned char* out, uint32_t row_of) {
+        unsigned char* const to = out + (uint64_t(row_of) * channels + n) * E;
+        if (left_n >= VE) {
+          V::store(to, v);
+        } else {
+#pragma unroll
+          for (uint32_t e = 0; e + 1 < VE; ++e)
+            if (e < left_n) One::store(to + e * E, v[e * E / 4] >> (e * E % 4 * 8));
+        }
+      };
+      if (a.form <= 1) {
+        put(a.out[own], t);
+      } else if (a.form == 2) {
+        for (int r2 = 0; r2 < a.P; ++r2) put(a.out[r2], t);
+      } else {
+        put(a.out[t / a.row_seg], t % a.row_seg);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // ---- tiles at any alignment
 
 // A tile of TT tokens by TN channels of WT by WN waves, whose rows may begin and
 // end anywhere: 128 codes of each at a time through registers into one of two
-// halves of LDS, the next on their way while one is multiplied.
+// halves of LDS, the next of them on their way while one is multiplied.
+constexpr uint32_t kAhead = 4;
+
 template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, bool SHORT>
 __global__ __launch_bounds__(64 * WT * WN) void product_tiles(ProductArgs a) {
   constexpr uint32_t WAVES = WT * WN, ROWS = TT + TN, EACH = ROWS / 8 / WAVES;  // rows of a thread's loads
@@ -222,6 +296,7 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles(ProductArgs a) {
   const auto open = [&]() {
     const uint64_t lo = dealt ? 0 : uint64_t(rank) * a.inner_seg;
     inner = rank >= end || lo >= a.inner ? 0 : dealt ? a.inner : min(a.inner_seg, a.inner - static_cast<uint32_t>(lo));
+    if (SHORT && a.form >= 2) inner = rank == 0 ? a.inner : 0;  // all ranks' codes of a row, one rank after the other
     k = 0;
   };
   const uint32_t row = wave * 8 + lane / 8, chunk = lane % 8;
@@ -241,10 +316,13 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles(ProductArgs a) {
       const bool is_x = j * 8 * WAVES < TT;
       const uint32_t r = j * 8 * WAVES + row - (is_x ? 0 : TT);
       // rows past the last one repeat it: their results are not stored
-      const unsigned char* const from = is_x ? a.x[rank] + uint64_t(t0) * inner : a.w[rank] + uint64_t(n0) * inner;
-      const uint32_t off = (is_x ? min(r, a.rows - 1 - t0) : min(r, channels - 1 - n0)) * inner;
-      if constexpr (SHORT) c.v[j] = short_row(from + off, inner, at);
-      else c.v[j] = *reinterpret_cast<const i32x4_any*>(from + (off + at));
+      const uint32_t of = is_x ? min(r, a.rows - 1 - t0) : min(r, channels - 1 - n0);
+      if constexpr (SHORT) {
+        c.v[j] = short_chunk(a, is_x ? a.x : a.w, (is_x ? t0 : n0) + of, rank, inner, at);
+      } else {
+        const unsigned char* const from = is_x ? a.x[rank] + uint64_t(t0) * inner : a.w[rank] + uint64_t(n0) * inner;
+        c.v[j] = *reinterpret_cast<const i32x4_any*>(from + (of * inner + at));
+      }
     }
     k += 128;
     if (k >= inner) {
@@ -282,35 +360,25 @@ __global__ __launch_bounds__(64 * WT * WN) void product_tiles(ProductArgs a) {
   // the codes still on their way to registers.
   const auto meet = []() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
   open();
-  Codes first, second;
-  load(first);
-  load(second);
-  if (first.any) put(halves[0], first);
+  Codes c[kAhead];
+#pragma unroll
+  for (uint32_t s = 0; s < kAhead; ++s) load(c[s]);
+  bool more = c[0].any;  // a rank may hold none of the inner width
+  if (more) put(halves[0], c[0]);
   meet();
-  bool more = first.any;  // a rank may hold none of the inner width
-  while (more) {          // halves[0] holds the codes to multiply, `second` the next ones, `first` is free
-    load(first);
-    multiply(halves[0]);
-    if (!second.any) break;
-    put(halves[1], second);
-    meet();
-    load(second);
-    multiply(halves[1]);
-    more = first.any;
-    if (more) put(halves[0], first);
-    meet();
-  }
+  while (more) {
 #pragma unroll
-  for (uint32_t i = 0; i < FT; ++i) {
-    const uint32_t t = t0 + wt + i * 16 + lane % 16;
-    if (t >= a.rows) continue;
-    const float xs = a.x_scale[t];
-#pragma unroll
-    for (uint32_t j = 0; j < FN; ++j) {
-      const uint32_t n = n0 + wn + j * 16 + lane / 16 * 4;
-      if (n < channels) store_results<DT>(a, own, channels, t, n, acc[i][j], xs);
+    for (uint32_t s = 0; s < kAhead; ++s) {  // halves[s % 2] holds the codes to multiply, c[s] is free, the others hold the next
+      load(c[s]);
+      multiply(halves[s % 2]);
+      more = c[(s + 1) % kAhead].any;
+      if (!more) break;
+      put(halves[(s + 1) % 2], c[(s + 1) % kAhead]);
+      meet();
     }
   }
+  meet();
+  store_tile<DT, FT, FN, sizeof(halves) / WAVES>(a, own, channels, t0 + wt, n0 + wn, acc, halves[0] + wave * (sizeof(halves) / WAVES), lane);
 }
 
 // ---- tiles of aligned rows
@@ -467,69 +535,13 @@ __global__ __launch_bounds__(64 * WT * WN) void product_wide(ProductArgs a) {
   // nothing on its way to LDS, and every stage read by all
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  // Results go through LDS, a part of it for each wave, so that rows of a wave's
-  // channels are stored whole (128 bytes and more of a 256 by 256 tile's).
-  typedef Pack<DT, 16 / Width<DT>::bytes> V;
-  typedef Pack<DT, 1> One;
-  constexpr uint32_t E = V::E, VE = 16 / E, NW = TN / WN, PITCH = NW * E + 16, SHARE = STAGES * STAGE / WAVES;
-  constexpr uint32_t FITS = SHARE / PITCH / 16, BATCH = FITS >= FT ? FT : FITS >= FT / 2 ? FT / 2 : FITS >= FT / 4 ? FT / 4 : 1;
-  static_assert(FITS >= 1 && FT % BATCH == 0, "a batch of 16 rows at least");
-  unsigned char* const mine = stages + wave * SHARE;
-#pragma unroll
-  for (uint32_t i0 = 0; i0 < FT; i0 += BATCH) {
-#pragma unroll
-    for (uint32_t i = i0; i < i0 + BATCH; ++i) {
-      const uint32_t t = t0 + wt + i * 16 + lane % 16;
-      const float xs = a.x_scale[min(t, a.rows - 1)];
-#pragma unroll
-      for (uint32_t j = 0; j < FN; ++j) {
-        const uint32_t n = j * 16 + lane / 16 * 4;
-        float f[4];
-#pragma unroll
-        for (uint32_t e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i][j][e]) * xs * a.w_scale[own][min(n0 + wn + n + e, channels - 1)];
-        unsigned char* const to = mine + ((i - i0) * 16 + lane % 16) * PITCH + n * E;
-        if constexpr (DT == kF32) *reinterpret_cast<u32x4*>(to) = u32x4{f2u(f[0]), f2u(f[1]), f2u(f[2]), f2u(f[3])};
-        else *reinterpret_cast<u32x2*>(to) = u32x2{Pack<DT, 8>::narrow2(f[0], f[1]), Pack<DT, 8>::narrow2(f[2], f[3])};
-      }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    constexpr uint32_t CHUNKS_ROW = NW * E / 16;
-#pragma unroll
-    for (uint32_t c0 = 0; c0 < BATCH * 16 * CHUNKS_ROW; c0 += 64) {
-      const uint32_t c = c0 + lane, r = c / CHUNKS_ROW, n = n0 + wn + c % CHUNKS_ROW * VE, t = t0 + wt + i0 * 16 + r;
-      if (c0 + 64 > BATCH * 16 * CHUNKS_ROW && c >= BATCH * 16 * CHUNKS_ROW) continue;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(mine + r * PITCH + c % CHUNKS_ROW * 16);
-      if (t >= a.rows || n >= channels) continue;
-      const uint32_t left_n = channels - n;
-      const auto put = [&](unsigned char* out, uint32_t row_of) {
-        unsigned char* const to = out + (uint64_t(row_of) * channels + n) * E;
-        if (left_n >= VE) {
-          V::store(to, v);
-        } else {
-#pragma unroll
-          for (uint32_t e = 0; e + 1 < VE; ++e)
-            if (e < left_n) One::store(to + e * E, v[e * E / 4] >> (e * E % 4 * 8));
-        }
-      };
-      if (a.form <= 1) {
-        put(a.out[own], t);
-      } else if (a.form == 2) {
-        for (int r2 = 0; r2 < a.P; ++r2) put(a.out[r2], t);
-      } else {
-        put(a.out[t / a.row_seg], t % a.row_seg);
-      }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-  }
+  store_tile<DT, FT, FN, STAGES * STAGE / WAVES>(a, own, channels, t0 + wt, n0 + wn, acc, stages + wave * (STAGES * STAGE / WAVES), lane);
 }
 
-// ---- up to 16 tokens and few channels
+// ---- few results
 
-// The weights are read once and nothing else counts.  A workgroup takes 16 tokens
-// by 16 channels, so that few channels still fill the card; its waves take pieces
-// of the inner width in turn, 256 codes of every row straight from memory in the
+// Few tokens by few channels.  A workgroup takes 16 by 16 of them, so that few still
+// fill the card; its waves take pieces of the inner width in turn, 256 codes of every row straight from memory in the
 // layout that the matrix instruction reads, the next piece in flight while one is
 // multiplied, and their sums are joined through LDS.  Rows of 16 codes at least,
 // at any alignment (see keep_from).
@@ -541,7 +553,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
   constexpr uint32_t kPiece = 64 * kFewSteps;
   const bool dealt = a.form == 0;
   const uint32_t tiles_n = ((dealt ? a.channel_seg : a.channels) + 15) / 16;
-  const uint32_t tn = blockIdx.x % tiles_n, own = blockIdx.x / tiles_n;
+  const uint32_t tiles_t = (a.rows + 15) / 16, t0 = blockIdx.x % tiles_t * 16;
+  const uint32_t tn = blockIdx.x / tiles_t % tiles_n, own = blockIdx.x / tiles_t / tiles_n;
   const uint64_t before = uint64_t(own) * a.channel_seg;
   const uint32_t channels = !dealt ? a.channels : before < a.channels ? min(a.channel_seg, a.channels - static_cast<uint32_t>(before)) : 0;
   const uint32_t n0 = tn * 16;
@@ -551,7 +564,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
   const uint32_t r0 = a.form <= 1 ? own : 0;
   const uint32_t pieces = per_rank * (a.form <= 1 ? 1 : static_cast<uint32_t>(a.P));
   // tokens and channels past the last one repeat it: their results are not stored
-  const uint32_t row_t = min(lane % 16, a.rows - 1), row_n = min(lane % 16, channels - 1 - n0);
+  const uint32_t row_t = min(lane % 16, a.rows - 1 - t0), row_n = min(lane % 16, channels - 1 - n0);
   const auto inner_of = [&](uint32_t rank) {
     const uint64_t lo = dealt ? 0 : uint64_t(rank) * a.inner_seg;
     return dealt ? a.inner : lo < a.inner ? min(a.inner_seg, a.inner - static_cast<uint32_t>(lo)) : 0;
@@ -567,11 +580,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
       return;
     }
     const unsigned char* const w = a.w[rank] + uint64_t(n0) * inner;
+    const unsigned char* const x = a.x[rank] + uint64_t(t0) * inner;
 #pragma unroll
     for (uint32_t s = 0; s < kFewSteps; ++s) {
       const uint32_t k = min(k0 + s * 64 + lane / 16 * 16, inner - 16);
       c.w[s] = *reinterpret_cast<const i32x4_any*>(w + (row_n * inner + k));
-      c.x[s] = *reinterpret_cast<const i32x4_any*>(a.x[rank] + (row_t * inner + k));
+      c.x[s] = *reinterpret_cast<const i32x4_any*>(x + (row_t * inner + k));
     }
   };
   i32x4 acc = {0, 0, 0, 0};
@@ -608,7 +622,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void product_few(ProductArgs a) {
   i32x4 sum = part[0][lane];
 #pragma unroll
   for (uint32_t w = 1; w < kFewWaves; ++w) sum += part[w][lane];
-  const uint32_t t = lane % 16, n = n0 + lane / 16 * 4;
+  const uint32_t t = t0 + lane % 16, n = n0 + lane / 16 * 4;
   if (t < a.rows && n < channels) store_results<DT>(a, own, channels, t, n, sum, a.x_scale[t]);
 }
 
@@ -690,12 +704,14 @@ hipError_t launch(const ProductArgs& a, hipStream_t stream) {
   // Kinds of tiles by their time: us for a round of 256 of them over 8192 codes (so
   // much for the first round).  A large tile does more with what it reads, small ones
   // fill the card sooner.
+  const bool whole = whole_chunks(a);
   const auto rounds = [](uint64_t tiles) { return static_cast<double>((tiles + 255) / 256); };
   if (shortest < 16) {
-    launch_any<DT, 64, 64, 2, 2, true>(a, stream);
-  } else if (a.rows <= 16 && tiles_of(a, 16) <= 1024) {
+    if (tiles_of(a, 128) >= 512) launch_any<DT, 128, 128, 2, 4, true>(a, stream);
+    else launch_any<DT, 64, 64, 2, 2, true>(a, stream);
+  } else if (tiles_of(a, 16) <= (whole ? 256 : 512)) {
     launch_few<DT>(a, stream);
-  } else if (!whole_chunks(a)) {
+  } else if (!whole) {
     if (10 + 27 * rounds(tiles_of(a, 64)) <= 25 + 62 * rounds(tiles_of(a, 128))) launch_any<DT, 64, 64, 2, 2>(a, stream);
     else launch_any<DT, 128, 128, 2, 4>(a, stream);
   } else if (a.rows <= 32) {

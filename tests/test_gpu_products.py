@@ -299,3 +299,10 @@ def test_ranks_that_hold_none_of_the_inner_width(form, rows, inner, P):
     else:
         for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
             ref.check(got, x.want, 3, form)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("rows,inner,channels,P", [(3, 91, 517, 12), (300, 67, 200, 8), (129, 180, 130, 12), (40, 15, 70, 16), (5, 240, 33, 16)])
+def test_ranks_with_fewer_than_16_codes(form, dtype, rows, inner, channels, P):
+    Layer(rows, inner, channels, dtype).run(form, P)
