@@ -4,6 +4,13 @@
 // The sum over the inner width is a sum of whole numbers: exact in 32 bits
 // whatever its order, so where the inner width is dealt out to the ranks the
 // ranks' partial sums go into one accumulator and their AllReduce costs nothing.
+//
+// Kernels by what bounds them: many tokens, the matrix cores and what feeds them
+// (product_wide, aligned rows; product_tiles, any others); few tokens, the weights'
+// bytes (the same in narrow tiles); few results, the latency of a long sum
+// (product_few).  On one MI355X, sums of 8 ranks: 4096 tokens of 8192 codes by 4096
+// channels 106 us (2580 TOP/s; the vendor library's product of the same sizes 123),
+// 64 of 4096 by 131072 102 us (5.3 TB/s), 3 of 8192 by 4096 8.6 us (3.9 TB/s).
 #include <algorithm>
 
 #include "rowops.hpp"
@@ -57,8 +64,10 @@ __device__ __forceinline__ uint32_t wave_top(uint32_t x) {
 // once; a longer one (LONG) is read twice.  A rank's last vector ends with its
 // columns and overlaps its neighbour, which changes no maximum and writes the same
 // codes twice; VE is 1 where a rank has less than a vector.  No load waits behind a
-// branch.  inverse_of: 2^32 / a rank's pieces, rounded up: exact for the 128
-// pieces that are not LONG.
+// branch (behind one for each ragged end, each waited for the one before it).  HBM
+// bounds it: 4096 rows of 8192 bf16, 100 MB, 23 us on 8 ranks and 18 on one (4.4 and
+// 5.5 TB/s), 8192 rows 38 us (5.2 TB/s).  inverse_of: 2^32 / a rank's pieces, rounded
+// up: exact for the 128 pieces that are not LONG.
 template <int DT, int VE, uint32_t THREADS, uint32_t VECTORS, bool LONG>
 __global__ __launch_bounds__(THREADS) void quantize_rows(QuantizeArgs a, uint32_t inverse_of) {
   typedef Pack<DT, VE> V;
@@ -268,7 +277,10 @@ __device__ __forceinline__ void store_tile(const ProductArgs& a, uint32_t own, u
 
 // A tile of TT tokens by TN channels of WT by WN waves, whose rows may begin and
 // end anywhere: 128 codes of each at a time through registers into one of two
-// halves of LDS, the next of them on their way while one is multiplied.
+// halves of LDS, the next of them on their way while one is multiplied.  Loads of 16
+// bytes at odd addresses bound it: 4096 tokens of 8200 codes by 4096 channels, 8 ranks
+// of 1025 codes, 295 us, where 8192 codes through here take 196 and in tiles of aligned
+// rows 106.  981 tokens of 3038 codes by 461 channels 17 us.
 constexpr uint32_t kAhead = 4;
 
 template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, bool SHORT>
@@ -402,6 +414,17 @@ __device__ __forceinline__ void load_lds(i32x4 from, uint32_t at, uint32_t to) {
 
 constexpr uint32_t kWide = 128;  // codes of the inner width in a stage: a row of LDS
 
+// A tile of TT tokens by TN channels, WT by WN waves.  STAGES stages of 128 codes of
+// its rows lie in LDS, loaded there without a register between; a wave holds 64 codes
+// of its rows and multiplies them while it reads the next 64, so that neither the
+// loads, the reads nor the products wait for one another but at one barrier a stage.
+// 256 by 256 on 8 waves of 128 by 64, 4096 x 8192 x 4096: 106 us; 128 before reads and
+// products were taken in turn and 118 before rows were stored whole; with instructions of
+// 32 x 32 x 32 135 where 128; with stages of 64 codes, three to six, 127 to 139 where 118;
+// without its loads 84, without its reads of LDS 106, with neither 81.
+// TURN: each workgroup begins elsewhere in the inner width, so that those that stream
+// weights do not all ask for the same columns of their rows at once (64 x 4096 x 131072
+// 122 us without, 102 so; large tiles gain nothing).
 template <int DT, uint32_t TT, uint32_t TN, uint32_t WT, uint32_t WN, uint32_t STAGES, bool TURN>
 __global__ __launch_bounds__(64 * WT * WN) void product_wide(ProductArgs a) {
   constexpr uint32_t WAVES = WT * WN, ROWS = TT + TN, LOADS = ROWS / 8 / WAVES;  // a wave's loads of a stage, 8 rows each
@@ -541,10 +564,12 @@ __global__ __launch_bounds__(64 * WT * WN) void product_wide(ProductArgs a) {
 // ---- few results
 
 // Few tokens by few channels.  A workgroup takes 16 by 16 of them, so that few still
-// fill the card; its waves take pieces of the inner width in turn, 256 codes of every row straight from memory in the
-// layout that the matrix instruction reads, the next piece in flight while one is
-// multiplied, and their sums are joined through LDS.  Rows of 16 codes at least,
-// at any alignment (see keep_from).
+// fill the card; its waves take pieces of the inner width in turn, 256 codes of every
+// row straight from memory in the layout that the matrix instruction reads, the next
+// piece in flight while one is multiplied, and their sums are joined through LDS.  Rows
+// of 16 codes at least, at any alignment (see keep_from).  Latency bounds it; rows about
+// 1024 bytes apart, off alignment, also fall on one another in L1: 16 x 8200 x 256 on 8
+// ranks 38 us, 11112 codes 24.5.
 constexpr uint32_t kFewWaves = 16, kFewSteps = 4;
 
 template <int DT>
@@ -635,6 +660,10 @@ void launch(const QuantizeArgs& a, hipStream_t stream) {
   const uint64_t per_rank = (a.seg + uint64_t(64) * VE - 1) / (64 * VE), pieces = per_rank * ((a.width + a.seg - 1) / a.seg);
   const uint32_t by = static_cast<uint32_t>(std::min<uint64_t>(UINT32_MAX, ((uint64_t(1) << 32) + per_rank - 1) / per_rank));
   const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
+  // The fewest waves that hold a row (bf16 over 8 ranks, us): 4096 rows of 8192 in 4 waves
+  // 23, in 16 of four vectors 43, of eight 88; 2048 of 28672 in 16 of four 38, of eight 55,
+  // of 60000 in 16 of eight 85, read twice 93; 16384 rows of 512, one rank, in one wave 12,
+  // in four 22.
   if (pieces <= 4) dev::quantize_rows<DT, VE, 64, 4, false><<<grid, 64, 0, stream>>>(a, by);
   else if (pieces <= 16) dev::quantize_rows<DT, VE, 256, 4, false><<<grid, 256, 0, stream>>>(a, by);
   else if (pieces <= 64) dev::quantize_rows<DT, VE, 1024, 4, false><<<grid, 1024, 0, stream>>>(a, by);
@@ -701,27 +730,37 @@ void launch_wide(const ProductArgs& a, hipStream_t stream) {
 template <int DT>
 hipError_t launch(const ProductArgs& a, hipStream_t stream) {
   const uint32_t shortest = a.form == 0 ? a.inner : a.inner % a.inner_seg ? a.inner % a.inner_seg : a.inner_seg;
-  // Kinds of tiles by their time: us for a round of 256 of them over 8192 codes (so
-  // much for the first round).  A large tile does more with what it reads, small ones
-  // fill the card sooner.
+  // Times below are us, of 8 ranks.  A single round of small workgroups is left to
+  // product_few: 41 x 10496 x 1024 11.2 (in tiles of 64 by 32 20.5), 131 x 3989 x 28 9.3
+  // (64 by 64 19.9), 3 x 8192 x 4096 8.6 (32 by 32 11.5); two rounds are not, 16 x 4096 x
+  // 8192 11.2 (8.7), 512 x 3989 x 512 31 (21), but of one token at any alignment, whose
+  // lanes ask for one row: 1 x 4099 x 8190 16.0 (18.6).
   const bool whole = whole_chunks(a);
   const auto rounds = [](uint64_t tiles) { return static_cast<double>((tiles + 255) / 256); };
   if (shortest < 16) {
+    // 4096 x 100 x 4096 in tiles of 128 and 64 105 and 130; 1024 x 100 x 1024, 64 tiles of 128: 18.9 and 17.7
     if (tiles_of(a, 128) >= 512) launch_any<DT, 128, 128, 2, 4, true>(a, stream);
     else launch_any<DT, 64, 64, 2, 2, true>(a, stream);
-  } else if (tiles_of(a, 16) <= (whole ? 256 : 512)) {
+  } else if (tiles_of(a, 16) <= (whole || a.rows > 1 ? 256 : 512)) {
     launch_few<DT>(a, stream);
   } else if (!whole) {
+    // so much to begin with and for a round of 256 tiles: 1024 x 8200 x 4096 in tiles of 64 and 128 115 and 73, 512 tokens 62 and 70
     if (10 + 27 * rounds(tiles_of(a, 64)) <= 25 + 62 * rounds(tiles_of(a, 128))) launch_any<DT, 64, 64, 2, 2>(a, stream);
     else launch_any<DT, 128, 128, 2, 4>(a, stream);
   } else if (a.rows <= 32) {
-    if (tiles_of(a, 32, 64) >= 512) launch_wide<DT, 32, 64, 1, 4, 4, true>(a, stream);
+    // 16 x 4096 x 131072 in the first and the second 93 and 102 (tiles of 64 by 64 103), x 12288, 192 tiles, 10.3 and 11.2, x 8192 9.3 and 8.7
+    if (tiles_of(a, 32, 64) >= 192) launch_wide<DT, 32, 64, 1, 4, 4, true>(a, stream);
     else launch_wide<DT, 32, 32, 2, 2, 8>(a, stream);
   } else if (a.rows <= 64 && tiles_of(a, 64) <= 128) {
+    // more workgroups: 64 x 8192 x 4096 16.4, in tiles of 64 by 64 19.0; 64 x 4096 x 16384, 256 tiles of those, 13.9 in both
     launch_wide<DT, 64, 32, 2, 2, 4>(a, stream);
   } else if (a.rows <= 64 && tiles_of(a, 64, 256) >= 256) {
+    // the tokens read by fewer: 64 x 4096 x 65536 52 and x 131072 102, in tiles of 64 by 64 59 and 111; x 32768, 128 tiles, 33.9 and 32.7
     launch_wide<DT, 64, 256, 2, 4, 4, true>(a, stream);
   } else {
+    // us for a round of 256 tiles over 8192 codes (other widths scale all alike): x 8192
+    // x 4096 in tiles of 256, 128 and 64, 4096 tokens 106, 149 and 211, 2048 84, 74 and
+    // 104, 1024 83, 41 and 57, 512 82, 35 and 29, 256 -, 32 and 20
     const double large = 107 * rounds(tiles_of(a, 256)), middle = 38 * rounds(tiles_of(a, 128)), small = 4 + 13 * rounds(tiles_of(a, 64));
     if (small <= middle && small <= large) launch_wide<DT, 64, 64, 2, 2, 4>(a, stream);
     else if (middle <= large) launch_wide<DT, 128, 128, 2, 4, 4>(a, stream);
