@@ -332,3 +332,20 @@ def test_each_way_of_launching(pieces):
         g.clip(float(size) / 8, out, eps=0.0)
         near(out, size)
     ref.check(t.cpu(), (torch.full((n,), 0.0625).double(), torch.full((n,), 0.0625).double()), 2, "gradient")
+
+
+@pytest.mark.parametrize("norm_type", [1.0, 2.0, INF])
+def test_a_norm_of_more_than_the_caches_hold(norm_type):
+    """300 MB in three types, the norm alone and before clipping: the same bits."""
+    lengths = [40000001, 30000000, 29999999, 5]
+    held = []
+    for i, n in enumerate(lengths):
+        t = torch.randn(n, generator=torch.Generator("cuda").manual_seed(i), device="cuda")
+        held.append(t.to((F32, BF, F16, F32)[i]))
+    alone, before = number(), number()
+    size = step.norm([t.cpu() for t in held], norm_type)
+    with hc.Comm(4, "ring") as c, c.gradients(dealt=[[t] for t in held]) as g:
+        g.norm(alone, norm_type=norm_type)
+        near(alone, size)
+        g.clip(INF, before, norm_type=norm_type)
+    assert torch.equal(alone, before)

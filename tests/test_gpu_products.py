@@ -306,3 +306,19 @@ def test_ranks_that_hold_none_of_the_inner_width(form, rows, inner, P):
 @pytest.mark.parametrize("rows,inner,channels,P", [(3, 91, 517, 12), (300, 67, 200, 8), (129, 180, 130, 12), (40, 15, 70, 16), (5, 240, 33, 16)])
 def test_ranks_with_fewer_than_16_codes(form, dtype, rows, inner, channels, P):
     Layer(rows, inner, channels, dtype).run(form, P)
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("rows,inner,channels,P", [(2304, 256, 4096, 2), (1500, 100, 6000, 8), (1, 333, 5003, 3), (1, 90, 8170, 3),
+                                                   (2, 333, 4090, 1), (2, 333, 4100, 1), (30, 256, 12288, 1), (30, 256, 12200, 1)])
+def test_each_side_of_a_kind_of_tile(form, rows, inner, channels, P):
+    Layer(rows, inner, channels, BF).run(form, P)
+    x, out, call = aligned(rows, inner, channels, P, form)
+    with hc.Comm(P, "ring") as c:
+        call(c)
+    if form == "partial":
+        for (lo, hi), o in zip(ref.segments(inner, P), out):
+            ref.check(o, step.product(x.q[:, lo:hi], x.xs, x.w[:, lo:hi], x.ws), 3, form)
+    else:
+        for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
+            ref.check(got, x.want, 3, form)
