@@ -60,6 +60,8 @@ hbmc_status_t create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t t[], hbmc
     // that the others' vectors are aligned
     unsigned char* const base = static_cast<unsigned char*>(t[i].data[0]);
     uint64_t at = 0, most = kGradPieceBytes - reinterpret_cast<uintptr_t>(base) % 256;
+    const uint64_t more = bytes > most ? 1 + (bytes - most + kGradPieceBytes - 1) / kGradPieceBytes : 1;
+    if (more > kMaxGradPieces - pieces.size()) return HBMC_ERR_UNSUPPORTED;  // before a table of any length is made
     while (at < bytes) {
       const uint64_t here = std::min(most, bytes - at);
       p.data = base + at;
@@ -69,7 +71,6 @@ hbmc_status_t create(hbmc_comm_t comm, size_t n, const hbmc_gradient_t t[], hbmc
       at += here;
       most = kGradPieceBytes;
     }
-    if (pieces.size() > kMaxGradPieces) return HBMC_ERR_UNSUPPORTED;
   }
   if (!r.ok()) return HBMC_ERR_INVALID_ARG;
   std::sort(g->held.begin(), g->held.end());

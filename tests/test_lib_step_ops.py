@@ -4,6 +4,9 @@ before any device work) and of the Python binding, and the test references.
 """
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -187,3 +190,30 @@ def test_reference_norms_by_hand():
 def test_reference_codes_by_hand():
     q, s = step.codes(torch.tensor([[127.0, -63.0, 0.4], [0.0, 0.0, 0.0], [1.0, math.nan, 0.0]]))
     assert q.tolist() == [[127, -63, 0], [0, 0, 0], [0, 0, 0]] and s[:2].tolist() == [1.0, 0.0] and bool(s[2].isnan())
+
+
+# ------------------------------------------- limits met before memory is used
+
+LIMIT = """
+import ctypes, resource, sys
+import allreduce_reduction_amd as hc
+L = hc.load_library()
+comm = hc.Comm(4, "ring")
+used = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (used + (64 << 20), -1))
+table = (hc.Gradient * 2)()
+counts = [int(n) for n in sys.argv[1].split(",")]
+for i, n in enumerate(counts):
+    table[i] = hc.Gradient(n, 0, 1, (ctypes.c_void_p * 1)((i + 1) << 50))
+out = ctypes.c_void_p()
+print(L.hbmc_gradients_create(comm._h, len(counts), table, ctypes.byref(out)), out.value)
+"""
+
+
+@pytest.mark.parametrize("counts", [[2 ** 45], [2 ** 35 + 1], [4096, 2 ** 35 - 4095], [2 ** 47, 1]])
+def test_too_many_pieces_are_refused_before_they_are_made(counts):
+    """2^35 fp32 elements are the 2^23 pieces of 16 KiB that a handle holds; with 64
+    MiB more of memory than the library needs there is no room for their table."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", LIMIT, ",".join(map(str, counts))], cwd=root, capture_output=True, text=True, timeout=100)
+    assert r.stdout.split() == [str(UNSUPPORTED), "None"], (r.stdout, r.stderr)
