@@ -274,14 +274,18 @@ __global__ __launch_bounds__(kLogitThreads, 8) void adjust_logits(LogitArgs a) {
       if (!on[j]) continue;
       const uint32_t v = v0 + j * kLogitThreads;
       if (lists[j]) {
-        float f[VE];
         uint32_t w[VE];
         words_of(v, w);
-        V::widen(z[j], f);
+        // each alone: converting its neighbours too would set a signalling NaN's quiet bit
 #pragma unroll
-        for (uint32_t e = 0; e < VE; ++e)
-          if (w[e]) f[e] = adjust(f[e], w[e], p, sums);
-        z[j] = V::narrow(f);
+        for (uint32_t e = 0; e < VE; ++e) {
+          if (w[e] == 0) continue;
+          const uint32_t shift = e * E % 4 * 8, bits = E == 4 ? ~0u : 0xffffu << shift, at = e * E / 4;
+          float f[1];
+          One::widen(E == 4 ? z[j][at] : z[j][at] >> shift & 0xffffu, f);
+          f[0] = adjust(f[0], w[e], p, sums);
+          z[j][at] = (z[j][at] & ~bits) | One::narrow(f) << shift;
+        }
       }
       if (mask) {
         // -infinity over the forbidden columns' bits

@@ -242,3 +242,32 @@ def test_every_bias_names_one_column(in_place):
 @pytest.mark.parametrize("masked", [False, True])
 def test_most_biases_over_the_longest_tile(in_place, masked):
     Rows(190, 20000, BF, 12, 4095, masked).run(1, in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("dtype", [F32, F16, BF])
+def test_bits_beside_a_named_column(dtype, masked, in_place):
+    """Every other column a signalling NaN, whose quiet bit a conversion would
+    set, beside columns that tokens and biases name."""
+    rows, vocab, P = 5, 3001, 3
+    x = Rows(rows, vocab, dtype, 40, 6, masked)
+    ints, low, quiet = {F32: (torch.int32, 0x7f800000, 1 << 22), F16: (torch.int16, 0x7c00, 1 << 9), BF: (torch.int16, 0x7f80, 1 << 6)}[dtype]
+    g = torch.Generator().manual_seed(1)
+    nan = low + torch.randint(1, quiet, (rows, vocab), generator=g)
+    nan = nan - torch.where(torch.rand(rows, vocab, generator=g) < 0.5, 2 ** (8 * x.z.element_size() - 1), 0)  # either sign
+    named = torch.zeros(rows, vocab, dtype=torch.bool)
+    for r in range(rows):
+        for k in ("tokens", "bias_ids"):
+            at = x.kw[k][r]
+            named[r, at[(at >= 0) & (at < vocab)]] = True
+    bits = torch.where(named, x.z.view(ints).long(), nan).to(ints)
+    z = [guarded(bits[:, lo:hi].contiguous()) for lo, hi in ref.segments(vocab, P)]
+    out = z if in_place else [guarded(torch.zeros_like(t)) for t, _ in z]
+    with hc.Comm(P, "ring") as c:
+        c.adjust_logits([t.view(dtype) for t, _ in z], [t.view(dtype) for t, _ in out], **{k: v.cuda() for k, v in x.kw.items()})
+    got = torch.cat([t.cpu() for t, _ in out], 1)
+    kept = ~named & (step.allowed(x.kw["mask"], vocab) if masked else True)
+    assert int(kept.sum()) > 100
+    assert torch.equal(got[kept], bits[kept])
+    assert all(ok() for _, ok in z + out)
