@@ -627,7 +627,13 @@ class Gradients:
     """The gradients of a training step, for their global norm and clipping
     (see hbmc_gradients_create): made once for buffers that stay from step to
     step, and kept until close().  Tensors are contiguous, on the current device,
-    fp32, fp16 or bf16 in any mixture, and do not overlap."""
+    fp32, fp16 or bf16 in any mixture, and do not overlap.
+
+    The handle knows memory, not parameters: where a parameter's .grad is another
+    tensor in the next step, as after zero_grad() in its default form, the old one
+    is clipped and the new one is not.  Use zero_grad(set_to_none=False), or
+    gradients that are views of buffers of one's own.  Not made while a stream is
+    captured; its calls may be."""
 
     def __init__(self, comm: Comm, dealt=None, same=None):
         self._h = ctypes.c_void_p()

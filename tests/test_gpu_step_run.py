@@ -182,3 +182,36 @@ def test_dealt_out_gradients_clipped_where_they_lie():
     by = step.factor(size, 1.0)
     got = torch.cat([d[0].cpu() for d in dealt])
     ref.check(got, (total.double() * by, total.double().abs() * by), 2, "gradient")
+
+
+def test_training_steps_with_one_handle_of_gradients():
+    """A handle made after the first backward pass, whose gradients the next steps
+    fill again: zero_grad(set_to_none=False) leaves them where they are."""
+    g = torch.Generator().manual_seed(3)
+    shapes, steps = [(64, 33), (7, 64)], 3
+    params = [torch.randn(*s, generator=g).cuda().requires_grad_() for s in shapes]
+    twin = [p.detach().clone().requires_grad_() for p in params]
+    optimizer, plain = torch.optim.SGD(params, lr=0.1), torch.optim.SGD(twin, lr=0.1)
+    out, grads = torch.empty(1, device="cuda"), None
+    with hc.Comm(1, "ring") as c:
+        for _ in range(steps):
+            x = torch.randn(50, 33, generator=g).cuda()
+            for p, opt in ((params, optimizer), (twin, plain)):
+                opt.zero_grad(set_to_none=False)
+                (torch.tanh(x @ p[0].t()) @ p[1].t()).square().sum().backward()
+            before = [t.grad.cpu() for t in twin]
+            if grads is None:
+                grads = c.gradients(dealt=[[p.grad for p in params]])
+            grads.clip(1.0, out)
+            size = step.norm(before, 2.0)
+            by = step.factor(size, 1.0)
+            assert by < 1.0
+            # both sides' gradients are the same products of the same values
+            assert abs(float(out) - float(size)) <= 1.01 * 2.0 ** -24 * float(size)
+            for p, b, t in zip(params, before, twin):
+                ref.check(p.grad, (b.double() * by, b.double().abs() * by), 2, "gradient")
+                t.grad.copy_(p.grad)
+            optimizer.step()
+            plain.step()
+            assert same([p.detach() for p in params], [t.detach() for t in twin])
+        grads.close()
