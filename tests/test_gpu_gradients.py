@@ -349,3 +349,62 @@ def test_a_norm_of_more_than_the_caches_hold(norm_type):
         near(alone, size)
         g.clip(INF, before, norm_type=norm_type)
     assert torch.equal(alone, before)
+
+
+def phased(host, rank, whole):
+    """One rank's tensors of `host`, type by type packed in a buffer at a place of
+    the rank's own in 128 bytes (every third rank's is rank 0's); `whole`: with
+    their values.  The tensors, and the check of what lies around them."""
+    out, checks = [None] * len(host), []
+    for dt in sorted({t.dtype for t in host}, key=str):
+        mine = [i for i, t in enumerate(host) if t.dtype == dt]
+        total = sum(host[i].numel() for i in mine)
+        at = 64 + (5 * rank if rank % 3 else 0)
+        flat = torch.full((total + at + 70,), 7, dtype=dt, device="cuda")
+        for i, t in zip(mine, flat[at:at + total].split([host[i].numel() for i in mine])):
+            t.copy_(host[i]) if whole else t.zero_()
+            out[i] = t
+        checks.append(lambda flat=flat, at=at, total=total: bool((flat[:at] == 7).all()) and bool((flat[at + total:] == 7).all()))
+    return out, lambda: all(ok() for ok in checks)
+
+
+@pytest.mark.parametrize("norm_type", [2.0, INF])
+@pytest.mark.parametrize("P,times", [(1, 1), (2, 1), (2, 2), (11, 1)])
+def test_copies_of_thousands_of_pieces(P, times, norm_type):
+    """2260 pieces of 16 KiB and twice as many, whose scaling takes the factor from
+    a launch of its own; 74 MB written within the caches, 148 and 407 past them; more
+    than eight other copies."""
+    lengths = [n * times for n in (5000001, 2999999, 1, 2000003, 1500007, 1000, 1499993, 77)]
+    host = made(lengths, (BF, F32, F16), 10 * P + times)
+    held = [phased(host, r, r == 0) for r in range(P)]
+    assert sum(t.numel() * t.element_size() for t in host) > 2048 * 16384 * times
+    out = number()
+    size = step.norm(host, norm_type, 1.0 / P)
+    with hc.Comm(P, "ring") as c, c.gradients(same=[mine for mine, _ in held]) as g:
+        g.clip(0.3 * float(size), out, norm_type=norm_type, scale=1.0 / P, eps=0.0)
+    near(out, size)
+    by = step.factor(size, 0.3 * float(size), 1.0 / P, 0.0)
+    for t, h in zip(held[0][0], host):
+        v = h.double() * by
+        ref.check(t, (v, v.abs()), 2, "gradient")
+    for mine, ok in held:
+        assert all(torch.equal(a, b) for a, b in zip(mine, held[0][0])) and ok()
+
+
+@pytest.mark.parametrize("times", [1, 3])
+def test_dealt_shares_of_thousands_of_pieces(times):
+    """40 MB and 120 MB of random values dealt out, each rank's at a place of its own in 128 bytes."""
+    P = 3
+    host = made([n * times for n in (4000001, 2222221, 3000000, 1777, 2000003, 1111111)], (F32, BF, F16), times)
+    held = [phased(host[r::P], r, True) for r in range(P)]
+    out = number()
+    size = step.norm(host, 2.0)
+    with hc.Comm(P, "ring") as c, c.gradients(dealt=[mine for mine, _ in held]) as g:
+        g.clip(0.3 * float(size), out, eps=0.0)
+    near(out, size)
+    by = step.factor(size, 0.3 * float(size), 1.0, 0.0)
+    for r, (mine, ok) in enumerate(held):
+        for t, h in zip(mine, host[r::P]):
+            v = h.double() * by
+            ref.check(t, (v, v.abs()), 2, "gradient")
+        assert ok()
