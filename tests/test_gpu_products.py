@@ -322,3 +322,52 @@ def test_each_side_of_a_kind_of_tile(form, rows, inner, channels, P):
     else:
         for got in out if form == "reduce" else [torch.cat(out, 1 if form == "channels" else 0)]:
             ref.check(got, x.want, 3, form)
+
+
+def fenced(t, pad=64):
+    """A copy of t on the GPU, aligned as an allocator's, between guard zones, and their check."""
+    flat = torch.full((t.numel() + 2 * pad,), 7, dtype=t.dtype, device="cuda")
+    view = flat[pad:pad + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view, lambda: bool((flat[:pad] == 7).all()) and bool((flat[pad + t.numel():] == 7).all())
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("rows,inner,channels,P", [
+    (20, 512, 12301, 1),    # 32 by 64 of aligned rows
+    (30, 256, 12201, 1),    # 32 by 32
+    (50, 272, 8101, 1),     # 64 by 32
+    (64, 256, 65381, 1),    # 64 by 256
+    (64, 272, 16401, 1),    # 64 by 64
+    (2000, 640, 3001, 5),   # 128 by 128
+    (2304, 256, 4097, 2),   # 256 by 256, the ranks' own parts 128 by 128
+    (300, 333, 517, 3),     # 64 by 64 at any alignment
+    (1500, 333, 5001, 3),   # 128 by 128
+    (300, 67, 201, 8),      # 64 by 64 of ranks with fewer than 16 codes
+    (1500, 100, 6001, 8),   # 128 by 128
+])
+def test_types_in_each_kind_of_tile(form, dtype, rows, inner, channels, P):
+    """Whose results end inside 16 bytes, rows of them at odd addresses."""
+    x = Layer(rows, inner, channels, dtype)
+    cols = form == "channels"
+    q = [x.q.cuda()] * P if cols else [t.cuda() for t in split(x.q, P)]
+    w = [t.cuda() for t in (ref.split_rows(x.w, P) if cols else split(x.w, P))]
+    ws = [t.cuda() for t in ref.split_rows(x.ws, P)] if cols else x.ws.cuda()
+    zeros = lambda *s: fenced(torch.zeros(*s, dtype=dtype))  # noqa: E731
+    out = ([zeros(rows, len(t)) for t in w] if cols else
+           [zeros(len(t), channels) for t in ref.split_rows(x.xs, P)] if form == "scatter" else [zeros(rows, channels) for _ in range(P)])
+    with hc.Comm(P, "ring") as c:
+        if form in ("channels", "partial"):
+            c.product(q, x.xs.cuda(), w, ws, [t for t, _ in out])
+        else:
+            c.reduce_product(q, x.xs.cuda(), w, ws, [t for t, _ in out], scatter=form == "scatter")
+    if form == "partial":
+        for (lo, hi), (o, _) in zip(ref.segments(inner, P), out):
+            ref.check(o, step.product(x.q[:, lo:hi], x.xs, x.w[:, lo:hi], x.ws), 3, form)
+    elif form == "reduce":
+        ref.check(out[0][0], x.want, 3, form)
+        assert all(same([o], [out[0][0]]) for o, _ in out)
+    else:
+        ref.check(torch.cat([o for o, _ in out], 1 if cols else 0), x.want, 3, form)
+    assert all(ok() for _, ok in out)
