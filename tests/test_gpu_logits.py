@@ -271,3 +271,79 @@ def test_bits_beside_a_named_column(dtype, masked, in_place):
     assert int(kept.sum()) > 100
     assert torch.equal(got[kept], bits[kept])
     assert all(ok() for _, ok in z + out)
+
+
+def joined(ids, bias, vocab):
+    """The biases of each column added up in 32 bits, in list order."""
+    z = torch.zeros(ids.shape[0], vocab)
+    for r in range(ids.shape[0]):
+        seen = set()
+        for v, b in zip(ids[r].tolist(), bias[r]):
+            if 0 <= v < vocab:
+                z[r, v] = z[r, v] + b if v in seen else b
+                seen.add(v)
+    return z
+
+
+def repeated(kind, n, vocab, g):
+    """Places of a list of n biases that name columns again."""
+    ids = torch.randperm(vocab, generator=g)[:n]
+    if kind == "one":
+        ids[-1] = ids[0]
+    elif kind == "pairs":
+        ids[n // 2:2 * (n // 2)] = ids[:n // 2]
+    elif kind == "all":
+        ids[:] = ids[0]
+    elif kind == "few":
+        ids = ids[torch.randint(0, min(n, 7), (n,), generator=g)]
+    elif kind == "wrapping":  # places 5, 1000 and 3096, whose sum's low twelve bits are the first's; the last place of all
+        ids[999], ids[3095], ids[4094] = ids[4], ids[4], ids[7]
+    elif kind == "cancelling":  # the sums' low bits are none at all
+        ids[4094] = ids[0]
+    return ids
+
+
+@pytest.mark.parametrize("kind,n", [(k, n) for k in ("one", "pairs", "all", "few") for n in (2, 3, 65, 513, 1000)] +
+                         [(k, 4095) for k in ("one", "pairs", "all", "few", "wrapping", "cancelling")])
+@pytest.mark.parametrize("masked,in_place", [(False, True), (True, True), (False, False)])
+def test_repeated_biases_add_up_in_their_order(kind, n, masked, in_place):
+    """To zeros, so that the sums' bits are the results'; values whose order matters, in one tile and over several."""
+    g = torch.Generator().manual_seed(n)
+    rows, vocab, P = 3, 9000, 2
+    ids = torch.stack([repeated(kind, n, vocab, g), repeated(kind, n, vocab, g), torch.randint(-1, vocab, (n,), generator=g)])
+    bias = torch.randn(rows, n, generator=g) * torch.tensor([1.0, 1e4, 1e8])[torch.randint(0, 3, (rows, n), generator=g)]
+    on = torch.rand(rows, vocab, generator=g) < 0.7
+    want = joined(ids, bias, vocab)
+    if masked:
+        want[~on] = -torch.inf
+    z = [guarded(torch.zeros(rows, hi - lo)) for lo, hi in ref.segments(vocab, P)]
+    out = z if in_place else [guarded(torch.ones(rows, hi - lo)) for lo, hi in ref.segments(vocab, P)]
+    with hc.Comm(P, "ring") as c:
+        c.adjust_logits([t for t, _ in z], [t for t, _ in out], bias_ids=ids.cuda(), bias=bias.cuda(),
+                        mask=step.bits(on).cuda() if masked else None)
+    assert torch.equal(torch.cat([t.cpu() for t, _ in out], 1), want)
+    assert all(ok() for _, ok in z + out)
+
+
+def test_a_repeated_bias_costs_little():
+    """Once every bias of a tile with one repeated was compared with all others, which
+    took 250 times as long as distinct ones; twenty times is far from both."""
+    rows, n, vocab = 1, 4095, 8192
+    ids = torch.randperm(vocab, generator=torch.Generator().manual_seed(1))[None, :n]
+    again = ids.clone()
+    again[0, -1] = again[0, 0]
+    z, bias, took = [torch.zeros(rows, vocab, device="cuda")], torch.zeros(rows, n, device="cuda"), []
+    with hc.Comm(1, "ring") as c:
+        for names in (ids.cuda(), again.cuda()):
+            best = float("inf")
+            for _ in range(5):
+                start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                c.adjust_logits(z, bias_ids=names, bias=bias)
+                start.record()
+                for _ in range(20):
+                    c.adjust_logits(z, bias_ids=names, bias=bias)
+                end.record()
+                torch.cuda.synchronize()
+                best = min(best, start.elapsed_time(end))
+            took.append(best)
+    assert took[1] < 20 * took[0], took
