@@ -3,9 +3,10 @@
 //
 // No gradient can be scaled before the last has been read, so the data is passed
 // over twice: a launch leaves one partial sum a workgroup, and the next joins
-// them (every workgroup by itself, in the same order) and scales.  Sums are kept
-// in 64 bits, so that no square overflows, none is lost, and the norm is right to
-// the last bit of its 32 whatever the number of gradients.
+// them and scales: every workgroup by itself, in the same order, or with many
+// pieces (kGradJoined) by a factor that a launch between them leaves.  Sums are kept
+// in 64 bits, so that no square overflows, none is lost, and the norm is that of the
+// gradients rounded once to 32 whatever their number.
 //
 // HBM bounds large calls: 268 million fp32 gradients (1.07 GB) are gathered in 161 us
 // (6.6 TB/s) and clipped in 526 (6.1 TB/s over both reads and the writes); 8 copies of
@@ -119,8 +120,8 @@ struct Held {
     }
     if (last < count) Pack<DT, 1>::store(to + uint64_t(last) * V::E, single);
   }
-  // To a copy at another phase of 16 bytes than the piece, which lies in `lds`: its
-  // vectors are put together there, since stores that cross 16 bytes are slow (8
+  // To a copy at another place in a line of 128 bytes than the piece, which lies in
+  // `lds`: its vectors are put together there, since stores that cross 16 bytes are slow (8
   // copies of 48 million bf16 gradients, seven of them so: 234 us, and 176 so).
   template <int DT, bool STREAM>
   static __device__ __forceinline__ void store_shifted(unsigned char* to, const uint32_t* lds, uint32_t count, uint32_t t) {
@@ -147,8 +148,8 @@ struct Held {
     if (c < count) Pack<DT, 1>::store(to + uint64_t(c) * E, Pack<DT, 1>::load(reinterpret_cast<const unsigned char*>(lds) + c * E));
   }
   // To every copy of the piece, eight of their addresses at a time, the first of them
-  // in `to`.  With `lds`, by way of it where a copy lies at another phase (p.shifted:
-  // any does).
+  // in `to`.  With `lds`, by way of it where a copy lies at another place in a line
+  // (p.shifted: any does).
   template <int DT, bool STREAM>
   __device__ __forceinline__ void store_all(const GradPiece& p, unsigned char* const* others, uint32_t t, uint32_t* lds, Others to) const {
     constexpr uint32_t E = Width<DT>::bytes, VE = 16 / E;

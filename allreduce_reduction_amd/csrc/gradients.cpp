@@ -98,7 +98,7 @@ uint64_t workspace_of(const hbmc_gradients* g) {
   return sums ? (uint64_t(sums) + 1) * sizeof(double) : 0;
 }
 
-// Whether [p, p + bytes) is apart from every gradient and from the table.
+// Whether [p, p + bytes) is apart from every gradient.
 bool apart(const hbmc_gradients* g, const void* p, uint64_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p), hi = lo + bytes;
   const auto next = std::upper_bound(g->held.begin(), g->held.end(), std::make_pair(lo, UINTPTR_MAX));

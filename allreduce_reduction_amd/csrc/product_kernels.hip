@@ -8,9 +8,11 @@
 // Kernels by what bounds them: many tokens, the matrix cores and what feeds them
 // (product_wide, aligned rows; product_tiles, any others); few tokens, the weights'
 // bytes (the same in narrow tiles); few results, the latency of a long sum
-// (product_few).  On one MI355X, sums of 8 ranks: 4096 tokens of 8192 codes by 4096
-// channels 106 us (2580 TOP/s; the vendor library's product of the same sizes 123),
-// 64 of 4096 by 131072 102 us (5.3 TB/s), 3 of 8192 by 4096 8.6 us (3.9 TB/s).
+// (product_few).  On one MI355X, 8 ranks, calls one after the other: 4096 tokens of 8192
+// codes by 4096 channels, scattered by tokens, 106 to 110 us from box to box (2500 to
+// 2580 TOP/s; the vendor library's product of the same sizes 115 where this took 109);
+// 64 of 4096 by 131072, the channels dealt out, 102 us (5.3 TB/s); 3 of 8192 by 4096 so
+// 8.6 us (3.9 TB/s), their sum to all ranks 9.1.
 #include <algorithm>
 
 #include "rowops.hpp"
@@ -662,10 +664,14 @@ void launch(const QuantizeArgs& a, hipStream_t stream) {
   const uint64_t per_rank = (a.seg + uint64_t(64) * VE - 1) / (64 * VE), pieces = per_rank * ((a.width + a.seg - 1) / a.seg);
   const uint32_t by = static_cast<uint32_t>(std::min<uint64_t>(UINT32_MAX, ((uint64_t(1) << 32) + per_rank - 1) / per_rank));
   const uint32_t grid = static_cast<uint32_t>(std::min<uint64_t>(a.rows, 1 << 20));
-  // The fewest waves that hold a row (bf16 over 8 ranks, us): 4096 rows of 8192 in 4 waves
-  // 23, in 16 of four vectors 43, of eight 88; 2048 of 28672 in 16 of four 38, of eight 55,
-  // of 60000 in 16 of eight 85, read twice 93; 16384 rows of 512, one rank, in one wave 12,
-  // in four 22.
+  // The fewest waves of these that hold a row (bf16, us, 8 ranks unless said).  One wave or
+  // four: 16384 rows of 512 on one rank (1 piece) 12 and 21, of 2048 (4) 18 and 37, of 2560
+  // (5) - and 37.  Four or 16: 4096 rows of 8192 (16) 23 and 42, of 11008 (24) - and 44, of
+  // 16384 (32) - and 49.  16 of four vectors or of eight: 2048 rows of 28672 (56) 37 and 55,
+  // of 32768 (64) 40 and 58.  16 of eight or read twice: of 36864 (72) 60 and 55, of 60000
+  // (120) 85 and 92.  A piece past the row's last is the last one again, loaded and stored, so
+  // a row that just misses a kind pays for the next one whole: 4096 x 8200 57 where x 8192 23
+  // (eight waves of four would take 29, but are not among the kinds).
   if (pieces <= 4) dev::quantize_rows<DT, VE, 64, 4, false><<<grid, 64, 0, stream>>>(a, by);
   else if (pieces <= 16) dev::quantize_rows<DT, VE, 256, 4, false><<<grid, 256, 0, stream>>>(a, by);
   else if (pieces <= 64) dev::quantize_rows<DT, VE, 1024, 4, false><<<grid, 1024, 0, stream>>>(a, by);
@@ -740,7 +746,9 @@ hipError_t launch(const ProductArgs& a, hipStream_t stream) {
   const bool whole = whole_chunks(a);
   const auto rounds = [](uint64_t tiles) { return static_cast<double>((tiles + 255) / 256); };
   if (shortest < 16) {
-    // 4096 x 100 x 4096 in tiles of 128 and 64 105 and 130; 1024 x 100 x 1024, 64 tiles of 128: 18.9 and 17.7
+    // 4096 x 100 x 4096 in tiles of 128 and 64 105 and 130; 1024 x 100 x 1024, 64 tiles of 128: 18.9 and 17.7.
+    // Every rank's codes go one by one, also where the last alone has fewer than 16: 256 x 4548 x 4096
+    // over 64 ranks (72 each, 12) 420, x 4608 (72 each) 61; x 465 over 16 (30 each, 15) 55, x 480 18.
     if (tiles_of(a, 128) >= 512) launch_any<DT, 128, 128, 2, 4, true>(a, stream);
     else launch_any<DT, 64, 64, 2, 2, true>(a, stream);
   } else if (tiles_of(a, 16) <= (whole || a.rows > 1 ? 256 : 512)) {
@@ -760,9 +768,13 @@ hipError_t launch(const ProductArgs& a, hipStream_t stream) {
     // the tokens read by fewer: 64 x 4096 x 65536 52 and x 131072 102, in tiles of 64 by 64 59 and 111; x 32768, 128 tiles, 33.9 and 32.7
     launch_wide<DT, 64, 256, 2, 4, 4, true>(a, stream);
   } else {
-    // us for a round of 256 tiles over 8192 codes (other widths scale all alike): x 8192
-    // x 4096 in tiles of 256, 128 and 64, 4096 tokens 106, 149 and 211, 2048 84, 74 and
-    // 104, 1024 83, 41 and 57, 512 82, 35 and 29, 256 -, 32 and 20
+    // us for a round of 256 tiles over 8192 codes: x 8192 x 4096 in tiles of 256, 128 and
+    // 64, 4096 tokens 106, 149 and 211, 2048 84, 74 and 104, 1024 83, 41 and 57, 512 82, 35
+    // and 29, 256 -, 32 and 20.  Other widths do not scale by their codes alone, but keep the
+    // order: x 1024 26, 37 and 51; 23, 20 and 27; 22, 11 and 15; -, 9.9 and 8.3; -, 9.7 and
+    // 6.9; x 28672 362, 521 and 772; 322, 266 and 411; 329, 144 and 217; -, 128 and 118; -,
+    // 130 and 69.  So do results to all ranks (1024 tokens 98, 53 and 78) and the ranks' own
+    // parts (46, 61 and 82)
     const double large = 107 * rounds(tiles_of(a, 256)), middle = 38 * rounds(tiles_of(a, 128)), small = 4 + 13 * rounds(tiles_of(a, 64));
     if (small <= middle && small <= large) launch_wide<DT, 64, 64, 2, 2, 4>(a, stream);
     else if (middle <= large) launch_wide<DT, 128, 128, 2, 4, 4>(a, stream);

@@ -150,7 +150,7 @@ struct GradPiece {
   uint32_t dtype;
   uint32_t first;   // of the other copies' addresses
   uint16_t copies;  // buffers that hold the tensor, `data`'s included
-  uint16_t shifted; // whether any lies at another phase of 16 bytes
+  uint16_t shifted; // whether any lies at another place in a line of 128 bytes
 };
 
 struct GradArgs {
